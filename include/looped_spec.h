@@ -395,6 +395,113 @@ int lt_gemm_rows(int dtype, const void* d_w, const void* d_x, float* d_y, int n_
 int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y, int n_out,
                          int k, int ncols, void* stream);
 
+/*
+ * Serving operators: attention over whole prompts, attention of rows that
+ * share a prefix over the slot cache, and the verification of drafted tokens.
+ * They take the shapes of the models above (head_dim 32, 64, 96 or 128) and
+ * grouped heads: n_heads query heads, n_kv_heads key/value heads, query head h
+ * reads key/value head h / (n_heads / n_kv_heads), at most 64 query heads per
+ * key/value head.  dtype LT_BF16 (bf16 operands and weights of the products,
+ * fp32 scores, sums and outputs before the last rounding) or LT_F32 (fp32
+ * throughout).
+ *
+ * All three are asynchronous on `stream` (of the current device), allocate
+ * nothing, copy nothing from the host and may be captured in a CUDA graph:
+ * lengths and offsets are read on the device when the kernels run, so a
+ * replayed graph follows them.  A scratch buffer belongs to one call (or one
+ * captured graph) at a time; its contents need no initialisation.
+ * Offset arrays ("_off", device int32 [n + 1]) are ascending: entry i is
+ * off[i] .. off[i+1] - 1, empty entries are allowed.
+ * d_status (device int32, zeroed by the caller, may be NULL) receives the
+ * first device-side failure and keeps it: DEV_TIMEOUT (1) a bounded wait gave
+ * up, DEV_BAD_INDEX (4) offsets out of range or not ascending.  Nothing out of
+ * range is read or written in either case; the rows concerned are undefined.
+ */
+
+/*
+ * Causal attention over packed prompts (LoopSpec page, section 2.1: the
+ * prompt's pass through each layer's attention).  Sequence s has queries
+ * q_off[s] .. q_off[s+1]-1 and keys kv_off[s] .. kv_off[s+1]-1; the last
+ * query sees every key of its sequence, and each query before it one key
+ * less, so a prompt can be taken in pieces (more keys than queries).  Per
+ * query i and head h: o = sum_j softmax_j(scale * q_i . k_j) v_j over the keys
+ * it sees.  A query that sees no key (fewer keys than queries) gets zeros.
+ *   d_q, d_o  [n_q][n_heads][head_dim], token stride stride_q / stride_o elements
+ *   d_k, d_v  [n_kv][n_kv_heads][head_dim], token stride stride_k / stride_v;
+ *             q, k and v may be parts of one projection's rows
+ *   d_kv_off  NULL: q_off (keys are the queries' own tokens; n_kv = n_q)
+ * Rows of d_o outside the sequences are left as they were.  A key or value
+ * that a query does not see never reaches it, infinities and NaN included.
+ * Errors: LT_ERR_ARG (null pointer, negative size, bad dtype, scale not
+ * positive and finite, a stride below the row), LT_ERR_SHAPE (heads, head_dim,
+ * a base or stride that is not a multiple of 16 bytes, a grid over 2^31 tiles),
+ * LT_ERR_CAPACITY (scratch), LT_ERR_CUDA (launch).
+ */
+int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int n_heads, int n_kv_heads,
+                                 int head_dim, size_t* bytes);
+int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, const void* d_k,
+                   long long stride_k, const void* d_v, long long stride_v, void* d_o,
+                   long long stride_o, const int32_t* d_q_off, const int32_t* d_kv_off, int n_seqs,
+                   int n_q, int n_kv, int n_heads, int n_kv_heads, int head_dim, float scale,
+                   void* d_scratch, size_t scratch_bytes, int32_t* d_status, void* stream);
+
+/*
+ * Attention of a batch of rows that share long prefixes, over one plane of the
+ * slot cache (LoopSpec page, sections 2.2 and 2.4: the branches of a step
+ * attend to the committed prefix and to their own uncommitted positions).
+ * Rows row_off[g] .. row_off[g+1]-1 form group g.  Each of them attends to the
+ * slots prefix[prefix_off[g] .. prefix_off[g+1]-1], read once for the whole
+ * group, and to its own slots tail[tail_off[row] .. tail_off[row+1]-1] (a
+ * branch's ancestors and itself; a slot may stand in several rows' tails and
+ * more than once).  Slot indices outside 0 .. n_slots-1 (e.g. -1 padding) are
+ * skipped.  A row that sees no slot gets zeros.
+ *   d_q, d_o   [n_rows][n_heads][head_dim], row stride stride_q / stride_o elements
+ *   d_cache    [n_slots][K|V][n_kv_heads * head_dim]: one plane of lt_kv_pool
+ *   d_prefix   int32 [n_prefix]; d_tail int32 [n_tail]; n_prefix and n_tail are
+ *              the lengths of the arrays
+ *   d_tail_off int32 [n_rows + 1]
+ * Rows outside the groups are left as they were.  A value that a row does not
+ * see never reaches it, infinities and NaN included.
+ * Errors: as lt_attn_prompt; LT_ERR_SHAPE also for n_rows over 65535.
+ */
+int lt_attn_prefix_scratch_bytes(int dtype, int n_rows, int n_groups, int n_heads, int n_kv_heads,
+                                 int head_dim, size_t* bytes);
+int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, const void* d_cache, int n_slots,
+                   void* d_o, long long stride_o, const int32_t* d_row_off, int n_groups, int n_rows,
+                   const int32_t* d_prefix, const int32_t* d_prefix_off, int n_prefix,
+                   const int32_t* d_tail, const int32_t* d_tail_off, int n_tail, int n_heads,
+                   int n_kv_heads, int head_dim, float scale, void* d_scratch, size_t scratch_bytes,
+                   int32_t* d_status, void* stream);
+
+/*
+ * Verification of drafted tokens from given random numbers (LoopSpec page,
+ * section 2.2, Eqs. 2-4, for a batch of chains of drafts).  Chain s has the
+ * drafts x_i = draft[off[s] + i], i < k = off[s+1] - off[s].  Its target rows
+ * (processed distributions, as a readout gives them) are rows off[s] + s + i,
+ * i <= k, of d_p; its draft rows are rows off[s] + i of d_q, or one-hot when
+ * d_q is NULL.  In order, draft i is accepted if u_accept[off[s] + i] * q_i(x_i)
+ * < p_i(x_i) (strict, in exact arithmetic; one-hot: q_i(x_i) = 1).  At the first
+ * draft not accepted the next token is drawn from w = max(0, p_i - q_i) (the
+ * difference rounded to fp32; one-hot: p_i without x_i; from p_i if w has no
+ * mass); when all are accepted, from w = p_k.  The draw is the lowest token j
+ * with sum_{i<=j} w_i > u_draw[s] * sum_i w_i, sums in 64 bits.  Entries of w
+ * that are not positive and finite weigh nothing.  A draft outside 0 .. V-1
+ * (e.g. -1 padding) is not accepted.
+ *   d_p [n_drafts + n_seqs] rows, d_q [n_drafts] rows of V fp32, row strides in
+ *       elements; d_draft int32 [n_drafts], d_off int32 [n_seqs + 1]
+ *   d_u_accept fp32 [n_drafts], d_u_draw fp32 [n_seqs], in [0, 1)
+ *   d_n_accepted int32 [n_seqs]: accepted drafts (-1: bad offsets, and the
+ *       chain's tokens are left as they were)
+ *   d_tokens int32 [n_drafts + n_seqs]: chain s from off[s] + s on: its accepted
+ *       drafts, the drawn token (-1 if the row has no mass), then -1
+ * Errors: LT_ERR_ARG (null pointer, negative size, V <= 0, a stride below V),
+ * LT_ERR_CUDA (launch).
+ */
+int lt_verify_drafts(const float* d_p, long long stride_p, const float* d_q, long long stride_q,
+                     const int32_t* d_draft, const int32_t* d_off, int n_seqs, int n_drafts, int V,
+                     const float* d_u_accept, const float* d_u_draw, int32_t* d_n_accepted,
+                     int32_t* d_tokens, int32_t* d_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 
 import torch
@@ -134,6 +135,14 @@ def _declare(L):
     L.lt_profile_steps.argtypes = [_vp, _i, _i, ctypes.POINTER(ProfileC)]
     L.lt_profile_gemms.argtypes = [_vp, _i, ctypes.POINTER(ctypes.c_double)]
     L.lt_get_info.argtypes = [_vp, ctypes.POINTER(InfoC)]
+    ll = ctypes.c_longlong
+    L.lt_attn_prompt_scratch_bytes.argtypes = [_i] * 6 + [ctypes.POINTER(_sz)]
+    L.lt_attn_prompt.argtypes = [_i, _vp, ll, _vp, ll, _vp, ll, _vp, ll, _vp, _vp, _i, _i, _i, _i, _i,
+                                 _i, ctypes.c_float, _vp, _sz, _vp, _vp]
+    L.lt_attn_prefix_scratch_bytes.argtypes = [_i] * 6 + [ctypes.POINTER(_sz)]
+    L.lt_attn_prefix.argtypes = [_i, _vp, ll, _vp, _i, _vp, ll, _vp, _i, _i, _vp, _vp, _i, _vp, _vp, _i,
+                                 _i, _i, _i, ctypes.c_float, _vp, _sz, _vp, _vp]
+    L.lt_verify_drafts.argtypes = [_vp, ll, _vp, ll, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]
     L.lt_reset.argtypes = [_vp]
     L.lt_last_error.argtypes = [_vp]
     L.lt_last_error.restype = ctypes.c_char_p
@@ -230,6 +239,176 @@ def selftest_wait(stream=None) -> dict:
     out = np.zeros(3, dtype=np.int32)
     check(lib().lt_selftest_wait(out.ctypes.data_as(_ip), _stream(stream)), "lt_selftest_wait")
     return {"status": int(out[0]), "context_alive": bool(out[1]), "wait_ms": int(out[2])}
+
+
+# ---------------------------------------------------------------------------
+# serving operators
+# ---------------------------------------------------------------------------
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for work on `stream` (None: the device's current stream), taken
+    from that stream's pool, so that its reuse is ordered after the work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _launch(device, stream, what, fn, *args) -> None:
+    """fn(*args, stream handle) with `device` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index is None or device.index == torch.cuda.current_device():
+        check(fn(*args, stream.cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            check(fn(*args, stream.cuda_stream), what)
+
+
+def _attn_dtype(t: torch.Tensor) -> int:
+    assert t.dtype in (torch.float32, torch.bfloat16), t.dtype
+    return LT_F32 if t.dtype == torch.float32 else LT_BF16
+
+
+def _heads(t: torch.Tensor) -> None:
+    """[tokens][heads][head_dim] whose heads lie side by side in a token's row."""
+    assert t.dim() == 3 and (t.numel() == 0 or t.stride(2) == 1)
+    assert t.shape[1] <= 1 or t.numel() == 0 or t.stride(1) == t.shape[2]
+
+
+def _row(t: torch.Tensor) -> int:
+    """Stride between rows; a single row's own stride may be anything."""
+    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])
+
+
+def _off(t: torch.Tensor, device) -> int:
+    assert t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.device == device
+    assert t.numel() >= 1
+    return t.data_ptr()
+
+
+def _list(t: torch.Tensor, dtype, device) -> int:
+    assert t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.device == device
+    return t.data_ptr()
+
+
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    assert status.dtype == torch.int32 and status.numel() >= 1 and status.device == device
+    return status.data_ptr()
+
+
+def attn_prompt_scratch(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor,
+                        stream=None) -> torch.Tensor:
+    """Scratch memory for attn_prompt calls of these sizes (or fewer tokens and
+    sequences), on one stream or in one captured graph at a time."""
+    need = _sz()
+    check(lib().lt_attn_prompt_scratch_bytes(_attn_dtype(q), q.shape[0], q_off.numel() - 1, q.shape[1],
+                                             k.shape[1], q.shape[2], ctypes.byref(need)),
+          "lt_attn_prompt_scratch_bytes")
+    return _new(need.value, torch.uint8, q.device, stream)
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off: torch.Tensor,
+                kv_off: torch.Tensor = None, scale: float = None, out: torch.Tensor = None,
+                scratch: torch.Tensor = None, status: torch.Tensor = None,
+                stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts through lt_attn_prompt: q [n_q][H][hd],
+    k and v [n_kv][H_kv][hd] (token strides free), offsets device int32.  Sequence
+    s's last query sees all of its keys.  Rows of `out` outside the sequences
+    keep their values (an `out` made here has none there).  scale: 1/sqrt(hd)."""
+    assert q.is_cuda and k.device == v.device == q.device and q.dtype == k.dtype == v.dtype
+    _heads(q), _heads(k), _heads(v)
+    n_q, H, hd = q.shape
+    n_kv, Hk = k.shape[0], k.shape[1]
+    assert k.shape == v.shape and k.shape[2] == hd
+    assert kv_off is not None or n_kv == n_q
+    assert kv_off is None or kv_off.numel() == q_off.numel()
+    if out is None:
+        out = _new((n_q, H, hd), q.dtype, q.device, stream)
+    assert out.shape == q.shape and out.dtype == q.dtype and out.device == q.device
+    _heads(out)
+    if scratch is None:
+        scratch = attn_prompt_scratch(q, k, q_off, stream)
+    assert scratch.device == q.device and scratch.is_contiguous()
+    _launch(q.device, stream, "lt_attn_prompt", lib().lt_attn_prompt, _attn_dtype(q), _ptr(q), _row(q), _ptr(k), _row(k),
+            _ptr(v), _row(v), _ptr(out), _row(out), _off(q_off, q.device),
+            None if kv_off is None else _off(kv_off, q.device), q_off.numel() - 1, n_q, n_kv, H, Hk, hd,
+            hd ** -0.5 if scale is None else float(scale), _ptr(scratch),
+            scratch.numel() * scratch.element_size(), _status_ptr(status, q.device))
+    return out
+
+
+def attn_prefix_scratch(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor,
+                        stream=None) -> torch.Tensor:
+    """Scratch memory for attn_prefix calls of these sizes (or fewer rows and
+    groups), on one stream or in one captured graph at a time."""
+    need = _sz()
+    check(lib().lt_attn_prefix_scratch_bytes(_attn_dtype(q), q.shape[0], row_off.numel() - 1, q.shape[1],
+                                             cache.shape[2] // q.shape[2], q.shape[2],
+                                             ctypes.byref(need)), "lt_attn_prefix_scratch_bytes")
+    return _new(need.value, torch.uint8, q.device, stream)
+
+
+def attn_prefix(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor, prefix: torch.Tensor,
+                prefix_off: torch.Tensor, tail: torch.Tensor, tail_off: torch.Tensor,
+                scale: float = None, out: torch.Tensor = None, scratch: torch.Tensor = None,
+                status: torch.Tensor = None, stream=None) -> torch.Tensor:
+    """Attention of rows that share prefixes through lt_attn_prefix: q [n_rows][H][hd],
+    cache [n_slots][2][H_kv * hd] (one plane of Decoder.kv_pool), lists and offsets
+    device int32.  Group g's rows row_off[g]:row_off[g+1] attend to the slots
+    prefix[prefix_off[g]:prefix_off[g+1]]; row r also to tail[tail_off[r]:tail_off[r+1]].
+    Rows outside the groups keep their values in `out`.  scale: 1/sqrt(hd)."""
+    dev = q.device
+    assert q.is_cuda and cache.device == dev and q.dtype == cache.dtype
+    _heads(q)
+    n_rows, H, hd = q.shape
+    assert cache.dim() == 3 and cache.shape[1] == 2 and cache.is_contiguous()
+    assert cache.shape[2] % hd == 0
+    n_groups = row_off.numel() - 1
+    assert prefix_off.numel() == n_groups + 1 and tail_off.numel() == n_rows + 1
+    if out is None:
+        out = _new((n_rows, H, hd), q.dtype, dev, stream)
+    assert out.shape == q.shape and out.dtype == q.dtype and out.device == dev
+    _heads(out)
+    if scratch is None:
+        scratch = attn_prefix_scratch(q, cache, row_off, stream)
+    assert scratch.device == dev and scratch.is_contiguous()
+    _launch(dev, stream, "lt_attn_prefix", lib().lt_attn_prefix, _attn_dtype(q), _ptr(q), _row(q), _ptr(cache),
+            cache.shape[0], _ptr(out), _row(out), _off(row_off, dev), n_groups, n_rows,
+            _list(prefix, torch.int32, dev), _off(prefix_off, dev), prefix.numel(),
+            _list(tail, torch.int32, dev), _off(tail_off, dev), tail.numel(), H, cache.shape[2] // hd,
+            hd, hd ** -0.5 if scale is None else float(scale), _ptr(scratch),
+            scratch.numel() * scratch.element_size(), _status_ptr(status, dev))
+    return out
+
+
+def verify_drafts(p: torch.Tensor, q, drafts: torch.Tensor, off: torch.Tensor,
+                  u_accept: torch.Tensor, u_draw: torch.Tensor, status: torch.Tensor = None,
+                  stream=None):
+    """Verification of chains of drafts through lt_verify_drafts: p [n_drafts + n][V]
+    and q [n_drafts][V] (None: one-hot drafts) fp32 distributions with free row
+    strides, drafts int32 [n_drafts], off int32 [n + 1], uniforms fp32.  Returns
+    (n_accepted int32 [n], tokens int32 [n_drafts + n]: chain s from off[s] + s on
+    its accepted drafts, the drawn token, then -1)."""
+    dev = p.device
+    n, k = off.numel() - 1, drafts.numel()
+    assert p.is_cuda and p.dtype == torch.float32 and p.dim() == 2 and p.shape[0] == k + n
+    V = p.shape[1]
+    assert V == 1 or p.stride(1) == 1 or p.numel() == 0
+    if q is not None:
+        assert q.device == dev and q.dtype == torch.float32 and q.shape == (k, V)
+        assert V == 1 or q.stride(1) == 1 or k == 0
+    assert u_accept.numel() == k and u_draw.numel() == n
+    acc = _new(n, torch.int32, dev, stream)
+    tok = _new(k + n, torch.int32, dev, stream)
+    _launch(dev, stream, "lt_verify_drafts", lib().lt_verify_drafts, _ptr(p), max(_row(p), V),
+            _ptr(q) if q is not None and k else None, max(_row(q), V) if q is not None and k else V,
+            _list(drafts, torch.int32, dev), _off(off, dev), n, k, V,
+            _list(u_accept, torch.float32, dev), _list(u_draw, torch.float32, dev), _ptr(acc), _ptr(tok),
+            _status_ptr(status, dev))
+    return acc, tok
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,213 @@
+// Shared parts of the stand-alone attention operators (lt_attn_prompt,
+// lt_attn_prefix): which rows and keys a tile covers, the fp32 tile kernel's
+// arithmetic, and small host helpers.
+//
+// Query rows are packed: the G = n_heads / n_kv_heads query heads that read one
+// key/value head sit side by side in a tile, so that a key/value row is loaded
+// once for all of them.  Packed row r of a tile is (token or branch r / G,
+// head r % G within the group).
+#pragma once
+
+#include "common.cuh"
+
+namespace lt {
+
+constexpr int ATTN_MAX_GROUP = 64;  // query heads per key/value head (they share a 64-row tile)
+
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// The element range of entry i of an offset array, clamped into [0, n] and
+// ascending.  Offsets that had to be clamped are reported once in `status`.
+__device__ __forceinline__ int2 off_range(const int32_t* __restrict__ off, int i, int n, int* status) {
+  const int a = __ldg(off + i), b = __ldg(off + i + 1);
+  int2 r = {min(max(a, 0), n), min(max(b, 0), n)};
+  r.y = max(r.x, r.y);
+  if (r.x != a || r.y != b) set_err(status, DEV_BAD_INDEX);
+  return r;
+}
+
+// ---- one tile of attention in fp32 (256 threads, 64 packed rows x 64 keys) ----
+// The flash recurrence: with m the running row maximum and l the running sum,
+// a block of scores s gives m' = max(m, max s), p = exp(s - m'),
+// l' = l exp(m - m') + sum p, O' = O exp(m - m') + p V.  Thread (ty, tx) of a
+// 16 x 16 grid holds scores of rows 4 ty + i and keys tx + 16 j, and output
+// columns 2 tx + 32 c.  K and V share one buffer, so two CTAs fit an SM.
+constexpr int SIMT_M = 64, SIMT_N = 64, SIMT_THREADS = 256;
+
+template <int HD>
+struct SimtSmem {
+  float q[SIMT_M][HD + 4];
+  float kv[SIMT_N][HD + 4];  // pitch HD + 4: eight rows read as float4 touch all banks once
+  float p[SIMT_M][SIMT_N + 4];
+};
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+  return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Row state of one tile: 4 rows per thread, replicated over the 16 threads of a row.
+template <int HD>
+struct SimtState {
+  float m[4], l[4], o[4][HD / 16];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) o[i][c] = 0.f;
+    }
+  }
+};
+
+// Copies the tile's query rows (scaled) to shared memory; rows without a pointer are zero.
+template <typename T, int HD, typename RowPtr>
+__device__ __forceinline__ void simt_load_q(SimtSmem<HD>& sm, RowPtr row, float scale) {
+  for (int e = threadIdx.x; e < SIMT_M * (HD / 4); e += SIMT_THREADS) {
+    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
+    const T* p = row(r);
+    float4 v = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
+    *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
+  }
+}
+
+// O += P V of one block.  GUARD: a weight of 0 takes nothing from its value
+// row, so that an infinity or NaN in a key that the row does not see stays
+// out (0 * inf is NaN).
+template <int HD, bool GUARD>
+__device__ __forceinline__ void simt_pv(SimtSmem<HD>& sm, SimtState<HD>& st) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 4
+  for (int k = 0; k < SIMT_N; k += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.p[ty * 4 + i][k]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        const float2 v = *reinterpret_cast<const float2*>(&sm.kv[k + u][tx * 2 + 32 * c]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
+          const bool take = !GUARD || w != 0.f;
+          st.o[i][2 * c] = fmaf(w, take ? v.x : 0.f, st.o[i][2 * c]);
+          st.o[i][2 * c + 1] = fmaf(w, take ? v.y : 0.f, st.o[i][2 * c + 1]);
+        }
+      }
+  }
+}
+
+// One block of 64 keys: `key(j)` / `val(j)` give key j's rows or nullptr (a key
+// that no row sees: its value is zero, so that nothing of it reaches a row),
+// `seen(r, j)` whether packed row r sees key j; `masked` (uniform): some row may
+// not see some key of the block.
+template <typename T, int HD, typename KeyPtr, typename ValPtr, typename Seen>
+__device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, KeyPtr key, ValPtr val,
+                                           Seen seen, bool masked) {
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  __syncthreads();  // the previous block's V (and P) is consumed
+  for (int e = threadIdx.x; e < SIMT_N * (HD / 4); e += SIMT_THREADS) {
+    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
+    const T* p = key(r);
+    *reinterpret_cast<float4*>(&sm.kv[r][c]) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  float s[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < HD; d += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][d]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (!seen(r, tx + 16 * j)) s[i][j] = -INFINITY;
+      mx = fmaxf(mx, s[i][j]);
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float mn = fmaxf(st.m[i], mx);
+    const float ms = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p is 0
+    const float f = expf(st.m[i] - ms);
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = expf(s[i][j] - ms);
+      sum += p;
+      sm.p[r][tx + 16 * j] = p;
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    st.l[i] = st.l[i] * f + sum;
+    st.m[i] = mn;
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) st.o[i][c] *= f;
+  }
+  __syncthreads();  // P is complete and K consumed
+  for (int e = threadIdx.x; e < SIMT_N * (HD / 4); e += SIMT_THREADS) {
+    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
+    const T* p = val(r);
+    *reinterpret_cast<float4*>(&sm.kv[r][c]) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncthreads();
+  if (masked)
+    simt_pv<HD, true>(sm, st);
+  else
+    simt_pv<HD, false>(sm, st);
+}
+
+// ---- host helpers --------------------------------------------------------------
+inline bool attn_shape_ok(int n_heads, int n_kv_heads, int head_dim) {
+  if (head_dim != 32 && head_dim != 64 && head_dim != 96 && head_dim != 128) return false;
+  return n_kv_heads > 0 && n_kv_heads <= 1024 && n_heads > 0 && n_heads % n_kv_heads == 0 &&
+         n_heads / n_kv_heads <= ATTN_MAX_GROUP;
+}
+// Rows start on 16-byte boundaries (vector loads and TMA).
+inline bool attn_aligned(int dtype, const void* p, long long stride) {
+  return ((uintptr_t)p & 15) == 0 && (stride * (dtype == 0 ? 4 : 2)) % 16 == 0;
+}
+inline int attn_sm_count() {
+  static int cached[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return 148;
+  if (!cached[dev]) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cached[dev] = n > 0 ? n : 148;
+  }
+  return cached[dev];
+}
+
+}  // namespace lt

@@ -1,0 +1,222 @@
+// Attention of a batch of rows that share long prefixes over the slot cache:
+// the keys of a group's prefix are read once for all of its rows (the branches
+// of one committed prefix, or the samples of one prompt), and each row's own
+// tail is read for it alone.
+#include "../../include/looped_spec.h"
+#include "attn_prefix.cuh"
+
+namespace lt {
+
+// fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
+template <typename T, int HD>
+__global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs a) {
+  extern __shared__ __align__(16) char smem_raw[];
+  SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
+  __shared__ int slot[PREFIX_N];
+  const int tok = SIMT_M / a.group, group = a.group;
+  const long long U = prefix_total(a, tok);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = U;
+  const int ctas = prefix_ctas(U, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
+  const size_t width = (size_t)a.kv_heads * HD;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  PrefixPos pos;
+  pos.find(a, tok, lo);
+  for (long long u = lo; u < hi;) {
+    if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
+      set_err(a.status, DEV_BAD_INDEX);
+      return;
+    }
+    if (u == pos.u0) pos.publish(a, tok);
+    const int b0 = (int)(u - pos.u0), b1 = (int)min((long long)pos.nb, b0 + (hi - u));
+    const int rows = pos.nrow * group, h0 = pos.kh * group;
+    const T* q = (const T*)a.q + (size_t)pos.row0 * a.sq + (size_t)h0 * HD;
+    __syncthreads();  // the previous tile's queries are consumed
+    simt_load_q<T, HD>(sm, [&](int r) -> const T* {
+      return r < rows ? q + (size_t)(r / group) * a.sq + (r % group) * HD : nullptr;
+    }, a.scale);
+    int2 mine[4];  // tail entries of this thread's rows, as key indices of the tile
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      mine[i] = {0, 0};
+      if (r < rows) {
+        const int2 t = off_range(a.tail_off, pos.row0 + r / group, a.n_tail, a.status);
+        mine[i] = {pos.g.np + t.x - pos.tail.x, pos.g.np + t.y - pos.tail.x};
+      }
+    }
+    const int np = pos.g.np, nk = np + pos.tail.y - pos.tail.x;
+    const T* kc = (const T*)a.cache + (size_t)pos.kh * HD;
+    SimtState<HD> st;
+    st.clear();
+    for (int b = b0; b < b1; ++b) {
+      const int x0 = b * PREFIX_N;
+      __syncthreads();
+      if (threadIdx.x < PREFIX_N) {
+        const int x = x0 + threadIdx.x;
+        int s = -1;
+        if (x < np) s = __ldg(a.prefix + pos.g.p0 + x);
+        else if (x < nk) s = __ldg(a.tail + pos.tail.x + x - np);
+        slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
+      }
+      __syncthreads();
+      simt_block<T, HD>(
+          sm, st, [&](int j) -> const T* { return slot[j] >= 0 ? kc + (size_t)slot[j] * 2 * width : nullptr; },
+          [&](int j) -> const T* { return slot[j] >= 0 ? kc + ((size_t)slot[j] * 2 + 1) * width : nullptr; },
+          [&](int r, int j) {
+            const int2 m = mine[r & 3];
+            return slot[j] >= 0 && (x0 + j < np || (x0 + j >= m.x && x0 + j < m.y));
+          },
+          x0 + PREFIX_N > np);
+    }
+    const size_t part = (size_t)(blockIdx.x + pos.t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= rows) continue;
+      if (tx == 0) a.ml[part * SIMT_M + r] = make_float2(st.m[i], st.l[i]);
+      float* o = a.part + (part * SIMT_M + r) * HD;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c)
+        *reinterpret_cast<float2*>(o + tx * 2 + 32 * c) = make_float2(st.o[i][2 * c], st.o[i][2 * c + 1]);
+    }
+    u += b1 - b0;
+    if (u < hi) pos.next(a, tok);
+  }
+}
+
+// Merge of a row's partials: with M the largest m, o = sum_i e^(m_i - M) O_i /
+// sum_i e^(m_i - M) l_i.  One warp per (row, head).
+template <typename T, int HD, int MT>
+__global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int grid) {
+  const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (h >= a.heads) return;
+  // rows before the first group or behind the last one are left as they were
+  const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
+  if (row < first || row >= last) return;
+  const long long U = a.head[0];
+  const int4 rt = a.row_tab[row];
+  const int t = rt.x + (h / a.group) * rt.y, r = rt.z + h % a.group;
+  if (U <= 0 || t < 0 || t >= a.max_tiles || r < 0 || r >= MT) {  // rows that the offsets do not reach
+    set_err(a.status, DEV_BAD_INDEX);
+    return;
+  }
+  const int4 tt = a.tile_tab[t];
+  const long long u0 = (long long)(unsigned)tt.x | ((long long)tt.y << 32);
+  if (u0 < 0 || tt.z <= 0 || u0 + tt.z > U) {
+    set_err(a.status, DEV_BAD_INDEX);
+    return;
+  }
+  const int ctas = prefix_ctas(U, grid);
+  const int c0 = prefix_cta_of(u0, U, ctas), c1 = prefix_cta_of(u0 + tt.z - 1, U, ctas);
+  float M = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ml[(size_t)(c + t) * MT + r].x);
+  M = warp_max(M);
+  if (M == -INFINITY) M = 0.f;  // a row that sees nothing: its sum is 0
+  float l = 0.f, o[HD / 32];
+#pragma unroll
+  for (int i = 0; i < HD / 32; ++i) o[i] = 0.f;
+  for (int c = c0; c <= c1; ++c) {
+    const size_t p = (size_t)(c + t) * MT + r;
+    const float2 v = a.ml[p];
+    const float w = expf(v.x - M);
+    l += w * v.y;
+    const float* src = a.part + p * HD + lane * (HD / 32);
+#pragma unroll
+    for (int i = 0; i < HD / 32; ++i) o[i] = fmaf(w, src[i], o[i]);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = (T*)a.o + (size_t)row * a.so + (size_t)h * HD + lane * (HD / 32);
+#pragma unroll
+  for (int i = 0; i < HD / 32; ++i) dst[i] = from_f<T>(o[i] * inv);
+}
+
+template <typename T, int HD>
+static cudaError_t prefix_simt(const PrefixArgs& a, int grid, cudaStream_t st) {
+  cudaFuncSetAttribute(k_attn_prefix_simt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)sizeof(SimtSmem<HD>));
+  k_attn_prefix_simt<T, HD><<<grid, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
+  k_attn_prefix_merge<T, HD, SIMT_M><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t prefix_simt_hd(const PrefixArgs& a, int hd, int grid, cudaStream_t st) {
+  switch (hd) {
+    case 32: return prefix_simt<T, 32>(a, grid, st);
+    case 64: return prefix_simt<T, 64>(a, grid, st);
+    case 96: return prefix_simt<T, 96>(a, grid, st);
+    default: return prefix_simt<T, 128>(a, grid, st);
+  }
+}
+
+// Scratch layout: total, tile table, row table, (m, l) pairs, partial outputs.
+struct PrefixPlan {
+  int mt, grid;
+  long long max_tiles;
+  size_t tile_at, row_at, ml_at, part_at, bytes;
+};
+static PrefixPlan prefix_plan(int dtype, int n_rows, int n_groups, int n_heads, int n_kv_heads, int hd) {
+  PrefixPlan p;
+  const int group = n_heads / n_kv_heads;
+  p.mt = SIMT_M;
+  p.grid = 2 * attn_sm_count();
+  p.max_tiles = (long long)n_kv_heads * (n_rows / (p.mt / group) + (long long)n_groups);
+  const size_t slots = (size_t)p.max_tiles + p.grid;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  p.tile_at = 256;
+  p.row_at = p.tile_at + up((size_t)p.max_tiles * sizeof(int4));
+  p.ml_at = p.row_at + up((size_t)n_rows * sizeof(int4));
+  p.part_at = p.ml_at + up(slots * p.mt * sizeof(float2));
+  p.bytes = p.part_at + up(slots * p.mt * (size_t)hd * sizeof(float));
+  return p;
+}
+
+}  // namespace lt
+
+using namespace lt;
+
+extern "C" int lt_attn_prefix_scratch_bytes(int dtype, int n_rows, int n_groups, int n_heads,
+                                            int n_kv_heads, int head_dim, size_t* bytes) {
+  if (!bytes || (dtype != LT_F32 && dtype != LT_BF16) || n_rows < 0 || n_groups < 0) return LT_ERR_ARG;
+  if (!attn_shape_ok(n_heads, n_kv_heads, head_dim) || n_rows > 65535) return LT_ERR_SHAPE;
+  const PrefixPlan p = prefix_plan(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
+  if (p.max_tiles > (1 << 30)) return LT_ERR_SHAPE;
+  *bytes = p.bytes;
+  return LT_OK;
+}
+
+extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, const void* d_cache,
+                              int n_slots, void* d_o, long long stride_o, const int32_t* d_row_off,
+                              int n_groups, int n_rows, const int32_t* d_prefix,
+                              const int32_t* d_prefix_off, int n_prefix, const int32_t* d_tail,
+                              const int32_t* d_tail_off, int n_tail, int n_heads, int n_kv_heads,
+                              int head_dim, float scale, void* d_scratch, size_t scratch_bytes,
+                              int32_t* d_status, void* stream) {
+  size_t need = 0;
+  const int e = lt_attn_prefix_scratch_bytes(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim, &need);
+  if (e != LT_OK) return e;
+  if (n_slots < 0 || n_prefix < 0 || n_tail < 0 || !(scale > 0.f) || !(scale < INFINITY)) return LT_ERR_ARG;
+  if (n_rows == 0 || n_groups == 0) return LT_OK;
+  if (!d_q || !d_o || !d_row_off || !d_prefix_off || !d_tail_off || !d_scratch ||
+      (n_slots > 0 && !d_cache) || (n_prefix > 0 && !d_prefix) || (n_tail > 0 && !d_tail))
+    return LT_ERR_ARG;
+  const long long w = (long long)n_heads * head_dim;
+  if (stride_q < w || stride_o < w) return LT_ERR_ARG;
+  if (!attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_o, stride_o) ||
+      ((uintptr_t)d_cache & 15) || ((uintptr_t)d_scratch & 15))
+    return LT_ERR_SHAPE;
+  if (scratch_bytes < need) return LT_ERR_CAPACITY;
+  const PrefixPlan p = prefix_plan(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
+  char* s = (char*)d_scratch;
+  PrefixArgs a = {d_q, d_cache, d_o, stride_q, stride_o, d_row_off, d_prefix, d_prefix_off, d_tail,
+                  d_tail_off, n_groups, n_rows, n_slots, n_prefix, n_tail, n_heads, n_kv_heads,
+                  n_heads / n_kv_heads, scale, (long long*)s, (int4*)(s + p.tile_at),
+                  (int4*)(s + p.row_at), (float2*)(s + p.ml_at), (float*)(s + p.part_at),
+                  (int)p.max_tiles, d_status};
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t r = dtype == LT_F32 ? prefix_simt_hd<float>(a, head_dim, p.grid, st)
+                                        : prefix_simt_hd<__nv_bfloat16>(a, head_dim, p.grid, st);
+  return r == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+}

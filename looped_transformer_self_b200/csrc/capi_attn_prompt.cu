@@ -1,0 +1,162 @@
+// Causal attention over whole prompts: packed sequences of different lengths,
+// grouped heads, keys that may start before the queries (a prompt taken in
+// pieces).  Query t of a sequence with lq queries and lk keys sees keys
+// 0 .. lk - lq + t.
+#include "../../include/looped_spec.h"
+#include "attn_common.cuh"
+
+namespace lt {
+
+struct PromptArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  long long sq, sk, sv, so;  // elements between tokens
+  const int32_t* q_off;
+  const int32_t* kv_off;
+  int n_seqs, n_q, n_kv, heads, kv_heads, group;
+  float scale;
+  int* status;
+};
+
+// Tile `t` of the packed batch in units of `tok` tokens: its sequence and its
+// tile within that (from the last one down: the longest rows start first).
+// Run by a whole warp; false when there is no such tile.
+struct PromptTile {
+  int q0, lq, k0, lk, tile;
+};
+__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int t, int tok, PromptTile& out) {
+  const int lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
+    const int s = s0 + lane;
+    int2 r = {0, 0};
+    if (s < a.n_seqs) r = off_range(a.q_off, s, a.n_q, a.status);
+    const int n = cdiv(r.y - r.x, tok);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, incl > t);
+    if (here) {
+      const int w = __ffs(here) - 1;
+      int2 kr = {0, 0};
+      if (lane == w) kr = off_range(a.kv_off, s, a.n_kv, a.status);
+      out.q0 = __shfl_sync(0xffffffffu, r.x, w);
+      out.lq = __shfl_sync(0xffffffffu, r.y - r.x, w);
+      out.k0 = __shfl_sync(0xffffffffu, kr.x, w);
+      out.lk = __shfl_sync(0xffffffffu, kr.y - kr.x, w);
+      out.tile = __shfl_sync(0xffffffffu, incl - 1 - t, w);
+      return true;
+    }
+    t -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
+template <typename T, int HD>
+__global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prompt_simt(PromptArgs a) {
+  extern __shared__ __align__(16) char smem_raw[];
+  SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
+  const int kh = blockIdx.x % a.kv_heads, tok = SIMT_M / a.group;
+  PromptTile pt;
+  if (!prompt_tile(a, blockIdx.x / a.kv_heads, tok, pt)) return;
+  const int t0 = pt.tile * tok, nt = min(tok, pt.lq - t0), rows = nt * a.group;
+  const int ctx = pt.lk - pt.lq;  // keys before the first query
+  const int group = a.group, h0 = kh * group;
+  const T* q = (const T*)a.q + (size_t)(pt.q0 + t0) * a.sq + (size_t)h0 * HD;
+  const T* k = (const T*)a.k + (size_t)pt.k0 * a.sk + (size_t)kh * HD;
+  const T* v = (const T*)a.v + (size_t)pt.k0 * a.sv + (size_t)kh * HD;
+  simt_load_q<T, HD>(sm, [&](int r) -> const T* {
+    return r < rows ? q + (size_t)(r / group) * a.sq + (r % group) * HD : nullptr;
+  }, a.scale);
+  SimtState<HD> st;
+  st.clear();
+  const int see_first = ctx + t0 + 1, see_last = min(ctx + t0 + nt, pt.lk);  // keys of the first / last row
+  for (int b = 0; b < see_last; b += SIMT_N) {
+    simt_block<T, HD>(
+        sm, st, [&](int j) -> const T* { return b + j < see_last ? k + (size_t)(b + j) * a.sk : nullptr; },
+        [&](int j) -> const T* { return b + j < see_last ? v + (size_t)(b + j) * a.sv : nullptr; },
+        [&](int r, int j) { return b + j <= ctx + t0 + r / group && b + j < see_last; },
+        b + SIMT_N > see_first);
+  }
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+    if (r >= rows) continue;
+    const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : st.l[i] == 0.f ? 0.f : st.l[i];
+    T* o = (T*)a.o + (size_t)(pt.q0 + t0 + r / group) * a.so + (size_t)(h0 + r % group) * HD;
+#pragma unroll
+    for (int c = 0; c < HD / 32; ++c) {
+      o[tx * 2 + 32 * c] = from_f<T>(st.o[i][2 * c] * inv);
+      o[tx * 2 + 32 * c + 1] = from_f<T>(st.o[i][2 * c + 1] * inv);
+    }
+  }
+}
+
+template <typename T, int HD>
+static cudaError_t prompt_simt(const PromptArgs& a, cudaStream_t st) {
+  const int tok = SIMT_M / a.group;
+  const unsigned tiles = (unsigned)(a.n_q / tok + a.n_seqs);
+  cudaFuncSetAttribute(k_attn_prompt_simt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       (int)sizeof(SimtSmem<HD>));
+  k_attn_prompt_simt<T, HD><<<tiles * a.kv_heads, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t prompt_simt_hd(const PromptArgs& a, int hd, cudaStream_t st) {
+  switch (hd) {
+    case 32: return prompt_simt<T, 32>(a, st);
+    case 64: return prompt_simt<T, 64>(a, st);
+    case 96: return prompt_simt<T, 96>(a, st);
+    default: return prompt_simt<T, 128>(a, st);
+  }
+}
+
+}  // namespace lt
+
+using namespace lt;
+
+extern "C" int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int n_heads, int n_kv_heads,
+                                            int head_dim, size_t* bytes) {
+  if (!bytes || (dtype != LT_F32 && dtype != LT_BF16) || n_q < 0 || n_seqs < 0) return LT_ERR_ARG;
+  if (!attn_shape_ok(n_heads, n_kv_heads, head_dim)) return LT_ERR_SHAPE;
+  // the launch grid counts tiles of 64 / group tokens
+  if (((long long)n_q / (SIMT_M / (n_heads / n_kv_heads)) + n_seqs) * n_kv_heads > 0x7fffffff)
+    return LT_ERR_SHAPE;
+  *bytes = 256;
+  return LT_OK;
+}
+
+extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, const void* d_k,
+                              long long stride_k, const void* d_v, long long stride_v, void* d_o,
+                              long long stride_o, const int32_t* d_q_off, const int32_t* d_kv_off,
+                              int n_seqs, int n_q, int n_kv, int n_heads, int n_kv_heads, int head_dim,
+                              float scale, void* d_scratch, size_t scratch_bytes, int32_t* d_status,
+                              void* stream) {
+  if (dtype != LT_F32 && dtype != LT_BF16) return LT_ERR_ARG;
+  if (n_seqs < 0 || n_q < 0 || n_kv < 0 || !(scale > 0.f) || !(scale < INFINITY)) return LT_ERR_ARG;
+  if (!attn_shape_ok(n_heads, n_kv_heads, head_dim)) return LT_ERR_SHAPE;
+  size_t need = 0;
+  if (int e = lt_attn_prompt_scratch_bytes(dtype, n_q, n_seqs, n_heads, n_kv_heads, head_dim, &need)) return e;
+  if (n_seqs == 0 || n_q == 0) return LT_OK;
+  if (!d_q || !d_o || !d_q_off || !d_scratch || (n_kv > 0 && (!d_k || !d_v))) return LT_ERR_ARG;
+  const long long w = (long long)n_heads * head_dim, wk = (long long)n_kv_heads * head_dim;
+  if (stride_q < w || stride_o < w || stride_k < wk || stride_v < wk) return LT_ERR_ARG;
+  if (!attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_k, stride_k) ||
+      !attn_aligned(dtype, d_v, stride_v) || !attn_aligned(dtype, d_o, stride_o))
+    return LT_ERR_SHAPE;
+  if (scratch_bytes < need) return LT_ERR_CAPACITY;
+  PromptArgs a = {d_q, d_k, d_v, d_o, stride_q, stride_k, stride_v, stride_o, d_q_off,
+                  d_kv_off ? d_kv_off : d_q_off, n_seqs, n_q, n_kv, n_heads, n_kv_heads,
+                  n_heads / n_kv_heads, scale, d_status};
+  cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t e = dtype == LT_F32 ? prompt_simt_hd<float>(a, head_dim, st)
+                                        : prompt_simt_hd<__nv_bfloat16>(a, head_dim, st);
+  return e == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+}
