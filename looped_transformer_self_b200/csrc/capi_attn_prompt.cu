@@ -3,58 +3,9 @@
 // pieces).  Query t of a sequence with lq queries and lk keys sees keys
 // 0 .. lk - lq + t.
 #include "../../include/looped_spec.h"
-#include "attn_common.cuh"
+#include "attn_prompt_tc.cuh"
 
 namespace lt {
-
-struct PromptArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  void* o;
-  long long sq, sk, sv, so;  // elements between tokens
-  const int32_t* q_off;
-  const int32_t* kv_off;
-  int n_seqs, n_q, n_kv, heads, kv_heads, group;
-  float scale;
-  int* status;
-};
-
-// Tile `t` of the packed batch in units of `tok` tokens: its sequence and its
-// tile within that (from the last one down: the longest rows start first).
-// Run by a whole warp; false when there is no such tile.
-struct PromptTile {
-  int q0, lq, k0, lk, tile;
-};
-__device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int t, int tok, PromptTile& out) {
-  const int lane = threadIdx.x & 31;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    int2 r = {0, 0};
-    if (s < a.n_seqs) r = off_range(a.q_off, s, a.n_q, a.status);
-    const int n = cdiv(r.y - r.x, tok);
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
-    }
-    const unsigned here = __ballot_sync(0xffffffffu, incl > t);
-    if (here) {
-      const int w = __ffs(here) - 1;
-      int2 kr = {0, 0};
-      if (lane == w) kr = off_range(a.kv_off, s, a.n_kv, a.status);
-      out.q0 = __shfl_sync(0xffffffffu, r.x, w);
-      out.lq = __shfl_sync(0xffffffffu, r.y - r.x, w);
-      out.k0 = __shfl_sync(0xffffffffu, kr.x, w);
-      out.lk = __shfl_sync(0xffffffffu, kr.y - kr.x, w);
-      out.tile = __shfl_sync(0xffffffffu, incl - 1 - t, w);
-      return true;
-    }
-    t -= __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return false;
-}
 
 // fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
 template <typename T, int HD>
@@ -108,14 +59,10 @@ static cudaError_t prompt_simt(const PromptArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T>
-static cudaError_t prompt_simt_hd(const PromptArgs& a, int hd, cudaStream_t st) {
-  switch (hd) {
-    case 32: return prompt_simt<T, 32>(a, st);
-    case 64: return prompt_simt<T, 64>(a, st);
-    case 96: return prompt_simt<T, 96>(a, st);
-    default: return prompt_simt<T, 128>(a, st);
-  }
+template <int HD>
+static int prompt_any(int dtype, const PromptArgs& a, cudaStream_t st) {
+  if (dtype == LT_BF16) return prompt_tc<HD>(a, st);
+  return prompt_simt<float, HD>(a, st) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 }  // namespace lt
@@ -156,7 +103,10 @@ extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, co
                   d_kv_off ? d_kv_off : d_q_off, n_seqs, n_q, n_kv, n_heads, n_kv_heads,
                   n_heads / n_kv_heads, scale, d_status};
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = dtype == LT_F32 ? prompt_simt_hd<float>(a, head_dim, st)
-                                        : prompt_simt_hd<__nv_bfloat16>(a, head_dim, st);
-  return e == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+  switch (head_dim) {
+    case 32: return prompt_any<32>(dtype, a, st);
+    case 64: return prompt_any<64>(dtype, a, st);
+    case 96: return prompt_any<96>(dtype, a, st);
+    default: return prompt_any<128>(dtype, a, st);
+  }
 }
