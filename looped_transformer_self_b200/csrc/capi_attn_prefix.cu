@@ -3,7 +3,7 @@
 // of one committed prefix, or the samples of one prompt), and each row's own
 // tail is read for it alone.
 #include "../../include/looped_spec.h"
-#include "attn_prefix.cuh"
+#include "attn_prefix_mma.cuh"
 
 namespace lt {
 
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= rows) continue;
-      if (tx == 0) a.ml[part * SIMT_M + r] = make_float2(st.m[i], st.l[i]);
+      if (tx == 0) a.ml[part * SIMT_M + r] = make_float2(st.m[i] * 1.4426950408889634f, st.l[i]);
       float* o = a.part + (part * SIMT_M + r) * HD;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c)
@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
   }
 }
 
-// Merge of a row's partials: with M the largest m, o = sum_i e^(m_i - M) O_i /
-// sum_i e^(m_i - M) l_i.  One warp per (row, head).
+// Merge of a row's partials: with M the largest m, o = sum_i 2^(m_i - M) O_i /
+// sum_i 2^(m_i - M) l_i.  One warp per (row, head).
 template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int grid) {
   const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   for (int c = c0; c <= c1; ++c) {
     const size_t p = (size_t)(c + t) * MT + r;
     const float2 v = a.ml[p];
-    const float w = expf(v.x - M);
+    const float w = exp2f(v.x - M);
     l += w * v.y;
     const float* src = a.part + p * HD + lane * (HD / 32);
 #pragma unroll
@@ -132,22 +132,31 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   for (int i = 0; i < HD / 32; ++i) dst[i] = from_f<T>(o[i] * inv);
 }
 
-template <typename T, int HD>
-static cudaError_t prefix_simt(const PrefixArgs& a, int grid, cudaStream_t st) {
-  cudaFuncSetAttribute(k_attn_prefix_simt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+template <int HD>
+static cudaError_t prefix_f32(const PrefixArgs& a, int grid, cudaStream_t st) {
+  cudaFuncSetAttribute(k_attn_prefix_simt<float, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        (int)sizeof(SimtSmem<HD>));
-  k_attn_prefix_simt<T, HD><<<grid, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
-  k_attn_prefix_merge<T, HD, SIMT_M><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
+  k_attn_prefix_simt<float, HD><<<grid, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
+  k_attn_prefix_merge<float, HD, SIMT_M><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
   return cudaGetLastError();
 }
 
-template <typename T>
-static cudaError_t prefix_simt_hd(const PrefixArgs& a, int hd, int grid, cudaStream_t st) {
-  switch (hd) {
-    case 32: return prefix_simt<T, 32>(a, grid, st);
-    case 64: return prefix_simt<T, 64>(a, grid, st);
-    case 96: return prefix_simt<T, 96>(a, grid, st);
-    default: return prefix_simt<T, 128>(a, grid, st);
+template <int HD, int MT>
+static cudaError_t prefix_mma(const PrefixArgs& a, int grid, cudaStream_t st) {
+  using C = PrefixMma<HD, MT>;
+  cudaFuncSetAttribute(k_attn_prefix_mma<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  k_attn_prefix_mma<HD, MT><<<grid, C::THREADS, C::SMEM, st>>>(a);
+  k_attn_prefix_merge<__nv_bfloat16, HD, MT><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
+  return cudaGetLastError();
+}
+
+template <int HD>
+static cudaError_t prefix_any(int dtype, int mt, const PrefixArgs& a, int grid, cudaStream_t st) {
+  if (dtype == LT_F32) return prefix_f32<HD>(a, grid, st);
+  switch (mt) {
+    case 16: return prefix_mma<HD, 16>(a, grid, st);
+    case 32: return prefix_mma<HD, 32>(a, grid, st);
+    default: return prefix_mma<HD, 64>(a, grid, st);
   }
 }
 
@@ -161,6 +170,11 @@ static PrefixPlan prefix_plan(int dtype, int n_rows, int n_groups, int n_heads, 
   PrefixPlan p;
   const int group = n_heads / n_kv_heads;
   p.mt = SIMT_M;
+  if (dtype == LT_BF16) {
+    // the smallest tile that holds an average group's packed rows (a group may take several tiles)
+    const long long avg = (long long)group * n_rows / (n_groups > 0 ? n_groups : 1);
+    p.mt = avg <= 16 && group <= 16 ? 16 : avg <= 32 && group <= 32 ? 32 : 64;
+  }
   p.grid = 2 * attn_sm_count();
   p.max_tiles = (long long)n_kv_heads * (n_rows / (p.mt / group) + (long long)n_groups);
   const size_t slots = (size_t)p.max_tiles + p.grid;
@@ -216,7 +230,12 @@ extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, co
                   (int4*)(s + p.row_at), (float2*)(s + p.ml_at), (float*)(s + p.part_at),
                   (int)p.max_tiles, d_status};
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t r = dtype == LT_F32 ? prefix_simt_hd<float>(a, head_dim, p.grid, st)
-                                        : prefix_simt_hd<__nv_bfloat16>(a, head_dim, p.grid, st);
+  cudaError_t r;
+  switch (head_dim) {
+    case 32: r = prefix_any<32>(dtype, p.mt, a, p.grid, st); break;
+    case 64: r = prefix_any<64>(dtype, p.mt, a, p.grid, st); break;
+    case 96: r = prefix_any<96>(dtype, p.mt, a, p.grid, st); break;
+    default: r = prefix_any<128>(dtype, p.mt, a, p.grid, st); break;
+  }
   return r == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
