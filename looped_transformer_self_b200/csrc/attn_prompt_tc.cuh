@@ -1,18 +1,28 @@
 // lt_attn_prompt for bf16 on the 5th-generation tensor cores.
 //
-// One CTA takes two tiles of 128 packed query rows of one key/value head and
-// streams the keys they see in blocks of 128 through a ring of shared-memory
-// slots (TMA).  Warps 0-3 and 4-7 hold one tile each, a row per thread; warp 8
-// loads, warp 9 issues the MMAs.  Per tile and block:
+// One resident CTA per SM takes work items one after the other: two tiles of
+// 128 packed query rows of one key/value head, against the keys they see (or a
+// range of them, see `splits`), streamed in blocks of 128 through a ring of
+// shared-memory slots (TMA).  Warps 0-3 and 4-7 hold one tile each, a row per
+// thread; warp 8 loads, warps 9 and 10 issue the tiles' MMAs, warp 11 fetches
+// items.  Per tile and block:
 //   S = Q K^T      tcgen05.mma, both from shared memory, S in TMEM (fp32)
-//   P = e^(S - m)  in registers, bf16 into the TMEM columns S stood in
+//   P = 2^(S' - m) in registers, bf16 into the TMEM columns S stood in
 //   O += P V       tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 // The tensor core runs the other tile's products while one tile is in its
-// softmax.  O is only rescaled when a row's maximum has grown by more than 2^8
-// since its reference was taken (the weights stay below 2^8 and the sums are
-// fp32, so nothing overflows and the relative rounding of a weight is the same
-// at any scale); that is rare after the first blocks, so O stays in TMEM.
+// softmax.  P is handed over in quarters, so that its product starts while the
+// rest is still being computed.
+// O is only rescaled when a row's maximum has grown by more than 2^8 since its
+// reference was taken: weights stay below 2^8 and sums are fp32, so nothing
+// overflows and the relative rounding of a weight is the same at any scale.
+//
+// Items come from the launch grid itself: a CTA that is done cancels a CTA that
+// has not started and takes its place (clusterlaunchcontrol), which balances
+// items of different lengths and lets loads and the first product of the next
+// item run under the softmax and output of the last.
 #pragma once
+
+#include <type_traits>
 
 #include "attn_tc.cuh"
 #include "prompt_tile.cuh"
@@ -21,67 +31,205 @@ namespace lt {
 
 template <int HD>
 struct PromptTc {
-  static constexpr int NT = 2;                        // tiles of a CTA
   static constexpr int CHUNKS = (HD + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int TILE = CHUNKS * 128 * 128;     // bytes of a 128-row tile
   static constexpr int SLOTS = HD > 64 ? 5 : 8;       // ring slots (K and V blocks in turn)
   static constexpr int OCOLS = CHUNKS * 64;           // TMEM columns of an output tile
-  static constexpr int THREADS = NT * 128 + 128;      // two softmax warpgroups, one for loads and MMAs
-  static constexpr size_t SMEM = 1024 + (size_t)(NT + SLOTS) * TILE;
+  static constexpr int THREADS = 384;                 // two softmax warpgroups, one for the rest
+  static constexpr size_t TILES = (size_t)(2 + SLOTS) * TILE;  // queries, ring
 };
 
-struct PromptBars {
-  uint64_t q_full, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_done[2], fin;
+constexpr int PROMPT_ITEMS = 3;  // items handed over ahead
+
+struct PromptItem {
+  int q0, k0, lq, lk;       // the sequence
+  int tile, kh, split, idx; // its pair of tiles, head, key range, place of its partial
+};
+struct PromptSmem {
+  PromptItem item[PROMPT_ITEMS];
+  alignas(16) uint4 clc;  // answer of a cancel request
+  uint64_t clc_full, loaded;
+  uint64_t item_full[PROMPT_ITEMS], item_empty[PROMPT_ITEMS];
+  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2][4], o_done[2], turn[2], fin;
   uint32_t tmem;
   int abort_flag;
-  int poison;  // a masked block held an infinity or NaN among its values
+  int poison[4];  // by item: (its number + 1) once a masked block held an infinity or NaN among its values
 };
+
+template <int HD>
+constexpr size_t prompt_smem() { return PromptTc<HD>::TILES + sizeof(PromptSmem); }
+
+// What an item covers: per tile first token, tokens, key blocks of its range.
+struct PromptSpan {
+  int t0[2], nt[2], nb[2], n, jb;
+  __device__ __forceinline__ PromptSpan(const PromptItem& it, int tok, int splits) {
+    int full[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t0[i] = (it.tile * 2 + i) * tok;
+      nt[i] = max(0, min(tok, it.lq - t0[i]));
+      full[i] = nt[i] ? cdiv(max(0, it.lk - it.lq + t0[i] + nt[i]), 128) : 0;
+    }
+    const int chunk = cdiv(max(full[0], full[1]), splits);
+    jb = it.split * chunk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) nb[i] = max(0, min(full[i] - jb, chunk));
+    n = max(nb[0], nb[1]);
+  }
+};
+
+// 2^y for y <= 0 on the FMA pipe, two at a time: y = n + f with n the nearest
+// integer (taken by adding and subtracting 1.5 * 2^23), 2^f = 1 + f g(f) with g
+// of degree 4 fitted to the least relative error on [-1/2, 1/2] (2^-22.3 in
+// fp32), and n added to the exponent.  y below -126 counts as -126.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void exp2_fma(uint64_t y, float& e0, float& e1) {
+  float a, b;
+  unpack2(y, a, b);
+  y = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
+  const uint64_t t = add2(y, big);
+  const uint64_t nt = add2(t, nbig);
+  const uint64_t f = fma2(nt, pack2(-1.f, -1.f), y);
+  uint64_t p = fma2(pack2(0.001326472731307149f, 0.001326472731307149f), f,
+                    pack2(0.009671512991189957f, 0.009671512991189957f));
+  p = fma2(p, f, pack2(0.05550733581185341f, 0.05550733581185341f));
+  p = fma2(p, f, pack2(0.24022242426872253f, 0.24022242426872253f));
+  p = fma2(p, f, pack2(0.6931470036506653f, 0.6931470036506653f));
+  p = fma2(p, f, pack2(1.f, 1.f));
+  float p0, p1, t0, t1;
+  unpack2(p, p0, p1);
+  unpack2(t, t0, t1);
+  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+// 32 scores x of a row to weights 2^(x sl + nms), as bf16 pairs in the first half
+// of x, and their fp32 values added to `sum`; FMA of every eight pairs on the FMA pipe.
+#ifndef PROMPT_FMA
+#define PROMPT_FMA 2
+#endif
+template <int FMA>
+__device__ __forceinline__ void softmax_chunk(uint32_t* x, uint64_t sl2, uint64_t nms2, uint64_t* sum) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t y = fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl2, nms2);
+    float e0, e1;
+    if (i % 8 < FMA) {
+      exp2_fma(y, e0, e1);
+    } else {
+      unpack2(y, e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+    }
+    sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
+    x[i] = pack_bf16(e0, e1);
+  }
+}
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+// Asks for a CTA that has not started; the answer lands in `to` and completes 16 bytes on `bar`.
+__device__ __forceinline__ void clc_request(uint32_t to, uint32_t bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last answer has been read
+  mbar_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(to),
+      "r"(bar)
+      : "memory");
+}
+// The block index it gave, or -1.
+__device__ __forceinline__ int clc_answer(uint32_t at) {
+  uint32_t x, ok;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}\n"
+      : "=r"(x), "=r"(ok)
+      : "r"(at)
+      : "memory");
+  return ok ? (int)x : -1;
+}
 
 template <int HD>
 __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
     k_attn_prompt_tc(PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv) {
   using C = PromptTc<HD>;
-  extern __shared__ char smem_raw[];
-  __shared__ PromptBars sb;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kh = blockIdx.x % a.kv_heads, group = a.group, tok = 128 / group;
-  PromptTile pt;
-  if (!prompt_tile(a, blockIdx.x / a.kv_heads, C::NT * tok, pt)) return;
-  const int ctx = pt.lk - pt.lq;
-  // per tile: first token, tokens, keys its last row sees, key blocks
-  int t0[2], nt[2], nb[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    t0[i] = (pt.tile * 2 + i) * tok;
-    nt[i] = max(0, min(tok, pt.lq - t0[i]));
-    nb[i] = nt[i] ? cdiv(max(0, ctx + t0[i] + nt[i]), 128) : 0;
+  extern __shared__ __align__(1024) char smem_raw[];
+  PromptSmem& sb = *reinterpret_cast<PromptSmem*>(smem_raw + C::TILES);
+  if (smem_u32(smem_raw) & 1023) {  // swizzle atoms are 1024 bytes
+    set_err(a.status, DEV_STATE);
+    return;
   }
-  const int n = max(nb[0], nb[1]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = a.group, tok = 128 / group;
 
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t q_s = base, ring = base + C::NT * C::TILE;
-  const uint32_t q_full = smem_u32(&sb.q_full), fin = smem_u32(&sb.fin);
+  const uint32_t q_s = smem_u32(smem_raw), ring = q_s + 2 * C::TILE;
+  const uint32_t q_full = smem_u32(&sb.q_full), q_empty = smem_u32(&sb.q_empty), fin = smem_u32(&sb.fin);
   auto kv_full = [&](int s) { return smem_u32(&sb.kv_full[s]); };
   auto kv_empty = [&](int s) { return smem_u32(&sb.kv_empty[s]); };
   auto s_full = [&](int t) { return smem_u32(&sb.s_full[t]); };
-  auto p_full = [&](int t) { return smem_u32(&sb.p_full[t]); };
+  auto p_full = [&](int t, int c) { return smem_u32(&sb.p_full[t][c]); };
   auto o_done = [&](int t) { return smem_u32(&sb.o_done[t]); };
   volatile int* abort_flag = &sb.abort_flag;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(fin, 1);
+    mbar_init(q_empty, 2);
+    mbar_init(fin, 2);
+    mbar_init(smem_u32(&sb.clc_full), 1);
+    mbar_init(smem_u32(&sb.loaded), 1);
+    for (int s = 0; s < PROMPT_ITEMS; ++s) {
+      mbar_init(smem_u32(&sb.item_full[s]), 1);
+      mbar_init(smem_u32(&sb.item_empty[s]), 11);  // eight softmax warps, the loader, two MMA warps
+    }
     for (int s = 0; s < C::SLOTS; ++s) {
       mbar_init(kv_full(s), 1);
-      mbar_init(kv_empty(s), 1);
+      mbar_init(kv_empty(s), 2);  // both tiles
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 128);
+      for (int c = 0; c < 4; ++c) mbar_init(p_full(t, c), 4);  // four warps
       mbar_init(o_done(t), 1);
+      mbar_init(smem_u32(&sb.turn[t]), 4);  // four warps of the other tile
     }
     sb.abort_flag = 0;
-    sb.poison = 0;
+    for (int i = 0; i < 4; ++i) sb.poison[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) {
@@ -96,202 +244,354 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
   const uint32_t tmem = sb.tmem;
   auto s_col = [&](int t) { return tmem + (uint32_t)t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + (uint32_t)t * C::OCOLS; };
-  // use u of the ring: K_0, V_0, K_1, V_1, ...
+  // use u of the ring: K and V of the items' blocks in turn
   auto slot_of = [&](int u) { return u % C::SLOTS; };
   auto par_of = [&](int u) { return (uint32_t)(u / C::SLOTS) & 1; };
+  // the next item of this CTA (its `it`-th); false at the end
+  auto take = [&](int it, PromptItem& item) -> bool {
+    const int e = it % PROMPT_ITEMS;
+    if (!mbar_wait(smem_u32(&sb.item_full[e]), (uint32_t)(it / PROMPT_ITEMS) & 1, abort_flag)) return false;
+    item = sb.item[e];
+    return item.tile >= 0;
+  };
+  auto give_back = [&](int it) { mbar_arrive(smem_u32(&sb.item_empty[it % PROMPT_ITEMS])); };
 
   // 168 registers a thread at launch (3 warps per scheduler): the softmax warpgroups take 216, the
-  // third keeps 72 (216 + 216 + 72 = 3 * 168).
+  // last keeps 72 (216 + 216 + 72 = 3 * 168).
   if (warp >= 8) {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-   if (warp == 8) {
-    if (lane == 0 && n > 0) {
-      const int qt = (nt[0] > 0) + (nt[1] > 0);
-      mbar_expect_tx(q_full, (uint32_t)(qt * C::CHUNKS * tok * group * 128));
-      for (int t = 0; t < qt; ++t) {
-        tma_load_4d(q_s + t * C::TILE, &mq, 0, kh * group, pt.q0 + t0[t], 0, q_full);
-        if (HD == 96) tma_load_4d(q_s + t * C::TILE + 16384, &mq, 64, kh * group, pt.q0 + t0[t], 0, q_full);
-      }
-      int u = 0;
-      for (; u < 2 * n; ++u) {
-        const int s = slot_of(u);
-        if (u >= C::SLOTS && !mbar_wait(kv_empty(s), par_of(u) ^ 1, abort_flag)) break;
-        const CUtensorMap* m = (u & 1) ? &mv : &mk;
-        const int key = pt.k0 + (u >> 1) * 128;
-        mbar_expect_tx(kv_full(s), C::TILE);
-        tma_load_4d(ring + s * C::TILE, m, 0, kh, key, 0, kv_full(s));
-        if (HD == 96) tma_load_4d(ring + s * C::TILE + 16384, m, 64, kh, key, 0, kv_full(s));
-      }
-      if (*abort_flag) {  // copies in flight land before the CTA leaves
-        int none = 0;
-        mbar_wait(q_full, 0, &none);
-        for (int i = max(0, u - C::SLOTS); i < u; ++i) mbar_wait(kv_full(slot_of(i)), par_of(i), &none);
-      }
-    }
-   } else if (warp == 9) {
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t IS = attn_idesc(128, false), IO = attn_idesc(HD, true);
-      auto issue_s = [&](int t, int u) {
-        const uint32_t k = ring + slot_of(u) * C::TILE, q = q_s + t * C::TILE;
-#pragma unroll
-        for (int i = 0; i < HD / 16; ++i) {
-          const uint32_t at = (uint32_t)(i >> 2) * 16384 + (i & 3) * 32;
-          tc_mma<false>(s_col(t), smem_desc(q + at), smem_desc(k + at), IS, i > 0);
-        }
-        tc_commit(s_full(t));
-      };
-      auto issue_o = [&](int t, int u, bool acc) {
-        const uint32_t v = ring + slot_of(u) * C::TILE;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          tc_mma_ts(o_col(t), s_col(t) + i * 8, smem_desc_mn(v + i * 2048, 16384), IO, acc || i > 0);
-        tc_commit(o_done(t));
-      };
-      bool ok = mbar_wait(q_full, 0, abort_flag) && mbar_wait(kv_full(0), 0, abort_flag);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < 2; ++t)
-          if (nb[t] > 0) issue_s(t, 0);
-        tc_commit(kv_empty(0));
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int uv = 2 * j + 1, uk = 2 * j + 2;
-        for (int t = 0; ok && t < 2; ++t) {
-          if (j >= nb[t]) continue;
-          ok = mbar_wait(kv_full(slot_of(uv)), par_of(uv), abort_flag) &&
-               mbar_wait(p_full(t), j & 1, abort_flag);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      if (lane == 0) {
+        int u = 0, qn = 0;
+        bool ok = true;
+        PromptItem item;
+        for (int it = 0; ok && take(it, item); ++it) {
+          const PromptSpan sp(item, tok, a.splits);
+          const int ub = u;
+          for (; u < ub + 2 * sp.n; ++u) {
+            if (u == ub + 1) {  // the queries, behind the first key block
+              if (qn > 0 && !(ok = mbar_wait(q_empty, (uint32_t)(qn - 1) & 1, abort_flag))) break;
+              const int qt = (sp.nt[0] > 0) + (sp.nt[1] > 0);
+              mbar_expect_tx(q_full, (uint32_t)(qt * C::CHUNKS * tok * group * 128));
+              for (int t = 0; t < qt; ++t) {
+                const int at = item.q0 + sp.t0[t];
+                tma_load_4d(q_s + t * C::TILE, &mq, 0, item.kh * group, at, 0, q_full);
+                if (HD == 96) tma_load_4d(q_s + t * C::TILE + 16384, &mq, 64, item.kh * group, at, 0, q_full);
+              }
+              ++qn;
+            }
+            const int s = slot_of(u);
+            if (u >= C::SLOTS && !(ok = mbar_wait(kv_empty(s), par_of(u) ^ 1, abort_flag))) break;
+            const CUtensorMap* m = ((u - ub) & 1) ? &mv : &mk;
+            const int key = item.k0 + (sp.jb + ((u - ub) >> 1)) * 128;
+            mbar_expect_tx(kv_full(s), C::TILE);
+            tma_load_4d(ring + s * C::TILE, m, 0, item.kh, key, 0, kv_full(s));
+            if (HD == 96) tma_load_4d(ring + s * C::TILE + 16384, m, 64, item.kh, key, 0, kv_full(s));
+          }
           if (!ok) break;
-          tc_fence_after();
-          issue_o(t, uv, j > 0);
-          if (j + 1 < nb[t]) {
-            ok = mbar_wait(kv_full(slot_of(uk)), par_of(uk), abort_flag);
+          give_back(it);
+          mbar_arrive(smem_u32(&sb.loaded));
+        }
+        if (*abort_flag) {  // copies in flight land before the CTA leaves
+          int none = 0;
+          if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1, &none);
+          for (int i = max(0, u - C::SLOTS); i < u; ++i) mbar_wait(kv_full(slot_of(i)), par_of(i), &none);
+        }
+      }
+    } else if (warp < 11) {
+      // One warp per tile, so that neither tile's products wait for the other's weights.  The whole
+      // warp walks through the items and waits; one elected lane issues (a loop run by one lane alone
+      // cost up to 250 cycles per MMA here: its operands do not stay in uniform registers).  MMAs of
+      // one thread run in order, so S may be written over the P of the product before it.
+      constexpr uint32_t IS = attn_idesc(128, false), IO = attn_idesc(HD, true);
+      const int t = warp - 9;
+      // descriptors count 16-byte units: a step along an operand is an addition
+      const uint64_t dq = smem_desc(q_s + t * C::TILE), dk = smem_desc(ring), dv = smem_desc_mn(ring, 16384);
+      const uint32_t st = s_col(t), ot = o_col(t), s_bar = s_full(t), o_bar = o_done(t);
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return __all_sync(0xffffffffu, mbar_try_wait(bar, par)) ||
+               __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag));
+      };
+      int slot = 0, done = 0, qn = 0;
+      uint32_t ring_par = 0;
+      auto next_slot = [&] {
+        if (++slot == C::SLOTS) {
+          slot = 0;
+          ring_par ^= 1;
+        }
+      };
+      bool ok = true;
+      PromptItem item;
+      for (int it = 0; ok; ++it) {
+        ok = __all_sync(0xffffffffu, take(it, item));
+        if (!ok) break;
+        const PromptSpan sp(item, tok, a.splits);
+        __syncwarp();
+        if (lane == 0) give_back(it);
+        if (sp.n == 0) continue;
+        const int nb = t ? sp.nb[1] : sp.nb[0];
+        if (!(ok = wait(q_full, (uint32_t)qn & 1))) break;
+        ++qn;
+        // Step j: the product of block j - 1's weights, then S of block j.  A slot is given back by
+        // both tiles, used or not, and not before it is full: no tile gets a turn of the ring ahead.
+        int v_slot = 0;
+        uint32_t v_par = 0;
+        for (int j = 0; j <= sp.n; ++j) {
+          const int k_slot = slot;
+          const uint32_t k_par = ring_par;
+          if (j > 0 && !(ok = wait(kv_full(v_slot), v_par))) break;
+          if (j > 0 && j <= nb) {
+            const uint64_t v = dv + (uint32_t)(v_slot * (C::TILE >> 4));
+            const uint32_t par = (uint32_t)(done + j - 1) & 1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (!(ok = ok && wait(p_full(t, c), par))) break;
+              tc_fence_after();
+              if (elect_one()) {
+                tc_mma_ts(ot, st + c * 16, v + c * 256, IO, j > 1 || c > 0);
+                tc_mma_ts(ot, st + c * 16 + 8, v + c * 256 + 128, IO, 1);
+                if (c == 3) tc_commit(o_bar);
+              }
+              __syncwarp();
+            }
             if (!ok) break;
-            issue_s(t, uk);
+          }
+          if (j < sp.n) {
+            if (!(ok = wait(kv_full(k_slot), k_par))) break;
+            if (j < nb) {
+              tc_fence_after();
+              const uint64_t k = dk + (uint32_t)(k_slot * (C::TILE >> 4));
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < HD / 16; ++i) {
+                  const uint32_t at = ((uint32_t)(i >> 2) * 16384 + (i & 3) * 32) >> 4;
+                  tc_mma<false>(st, dq + at, k + at, IS, i > 0);
+                }
+                tc_commit(s_bar);
+              }
+              __syncwarp();
+            }
+            next_slot();
+          }
+          if (elect_one()) {
+            if (j > 0) tc_commit(kv_empty(v_slot));
+            if (j < sp.n) tc_commit(kv_empty(k_slot));
+            if (j + 1 == sp.n) tc_commit(q_empty);
+          }
+          __syncwarp();
+          if (j < sp.n) {
+            v_slot = slot;
+            v_par = ring_par;
+            next_slot();
           }
         }
-        if (!ok) break;
-        tc_commit(kv_empty(slot_of(uv)));
-        if (j + 1 < n) tc_commit(kv_empty(slot_of(uk)));
+        done += nb;
       }
-      if (!ok) {  // MMAs in flight end before TMEM is freed
+      if (*abort_flag) {  // MMAs in flight end before TMEM is freed
         int none = 0;
-        tc_commit(fin);
+        if (elect_one()) tc_commit(fin);
+        __syncwarp();
         mbar_wait(fin, 0, &none);
+        __syncwarp();
+      }
+    } else {
+      // An item is asked for when the loads of the one before are out: the ring holds two blocks or
+      // more then, which covers the answer, and no CTA takes work that another could start sooner.
+      int idx = blockIdx.x, it = 0;
+      bool ok = true;
+      const uint32_t clc = smem_u32(&sb.clc), clc_full = smem_u32(&sb.clc_full);
+      auto wait = [&](uint32_t bar, uint32_t par) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag)) != 0;
+      };
+      for (uint32_t asked = 0;; ++asked) {
+        PromptTile pt;
+        const int pair = idx / a.splits;
+        const bool have = idx >= 0 && prompt_tile(a, pair / a.kv_heads, 2 * tok, pt);
+        if (have || idx < 0) {
+          const int e = it % PROMPT_ITEMS;
+          if (it >= PROMPT_ITEMS)
+            ok = wait(smem_u32(&sb.item_empty[e]), (uint32_t)(it / PROMPT_ITEMS - 1) & 1);
+          if (!ok) break;
+          if (lane == 0) {
+            PromptItem item = {0, 0, 0, 0, -1, 0, 0, 0};
+            if (have) item = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, pair % a.kv_heads, idx % a.splits, idx};
+            sb.item[e] = item;
+            mbar_arrive(smem_u32(&sb.item_full[e]));
+          }
+          if (idx < 0 || !wait(smem_u32(&sb.loaded), (uint32_t)it & 1)) break;
+          ++it;
+        }
+        if (lane == 0) clc_request(clc, clc_full);
+        __syncwarp();
+        if (!wait(clc_full, asked & 1)) {  // nothing writes to shared memory after the CTA is gone
+          int none = 0;
+          mbar_wait(clc_full, asked & 1, &none);
+          break;
+        }
+        idx = clc_answer(clc);
+        __syncwarp();
       }
     }
-   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
-    const int tl = r / group;                         // token within the tile
-    const bool valid = tl < nt[t] && r < tok * group;
-    const int see = valid ? ctx + t0[t] + tl + 1 : 0;  // keys this row sees (may be <= 0)
-    const int see_first = ctx + t0[t] + 1;             // keys the tile's first row sees
-    const float sl = a.scale * 1.4426950408889634f;    // scores in log2 units
-    float m = -INFINITY, l = 0.f;                      // m: reference maximum of the raw scores
+    const int tl = r / group;                        // token within the tile
+    const float sl = a.scale * 1.4426950408889634f;  // scores in log2 units
+    const float slack = fminf(8.f / sl, 1e30f);
+    int ub = 0, done = 0;
     bool ok = true;
-    for (int j = 0; j < nb[t]; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(s_full(t), j & 1, abort_flag));
+    auto wait = [&](uint32_t bar, uint32_t par) {
+      return __all_sync(0xffffffffu, mbar_try_wait(bar, par)) ||
+             __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag));
+    };
+    // The tiles take turns with their exponentials, one turn per block of the item (a tile without the
+    // block passes): left alone they fall into step, both in their softmax and then both waiting for
+    // the tensor core.
+    int turns = 0;
+    const uint32_t my_turn = smem_u32(&sb.turn[t]), other_turn = smem_u32(&sb.turn[t ^ 1]);
+    auto take_turn = [&](int k) { return wait(my_turn, (uint32_t)(turns + k + (t ^ 1)) & 1); };
+    auto pass_turn = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(other_turn);
+    };
+    for (int it = 0; ok; ++it) {
+      PromptItem item;
+      ok = __all_sync(0xffffffffu, take(it, item));
       if (!ok) break;
-      tc_fence_after();
-      uint32_t x[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, x + c * 32);
-      tmem_wait_ld();
-      const bool masked = (j + 1) * 128 > see_first;
-      if (masked) {
-        const int lim = see - j * 128;
-#pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= lim) x[c] = 0xff800000u;  // -inf
-      }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(x[c]));
-      const bool grow = (mx - m) * sl > 8.f;  // false where both are -inf
-      if (j == 0) {
-        m = mx;
-      } else if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? ex2((m - mx) * sl) : 1.f;
-        if (grow) m = mx;
-        l *= f;
-        ok = __all_sync(0xffffffffu, mbar_wait(o_done(t), (j - 1) & 1, abort_flag));
-        if (!ok) break;
+      if (lane == 0) give_back(it);
+      const PromptSpan sp(item, tok, a.splits);
+      const int t0 = t ? sp.t0[1] : sp.t0[0], nt = t ? sp.nt[1] : sp.nt[0], nb = t ? sp.nb[1] : sp.nb[0];
+      const int ctx = item.lk - item.lq;
+      const bool valid = tl < nt && r < tok * group;
+      const int see = valid ? ctx + t0 + tl + 1 : 0;  // keys this row sees (may be <= 0)
+      const int see_first = ctx + t0 + 1;             // keys the tile's first row sees
+      float m = -INFINITY, l = 0.f;                   // m: reference maximum of the raw scores
+      for (int jj = 0; jj < nb; ++jj) {
+        const int j = sp.jb + jj, ph = done + jj;
+        if (!(ok = wait(s_full(t), ph & 1))) break;
         tc_fence_after();
+        uint32_t x[128];
 #pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(oc + c, o);
-          tmem_wait_ld();
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, x + c * 32);
+        tmem_wait_ld();
+        const bool masked = (j + 1) * 128 > see_first;
+        if (masked) {
+          const int lim = see - j * 128;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tmem_st32(oc + c, o);
-        }
-      }
-      const float ms = m == -INFINITY ? 0.f : m * sl;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float e0 = ex2(fmaf(__uint_as_float(x[c * 32 + 2 * i]), sl, -ms));
-          const float e1 = ex2(fmaf(__uint_as_float(x[c * 32 + 2 * i + 1]), sl, -ms));
-          sum[i & 3] += e0 + e1;
-          p[i] = pack_bf16(e0, e1);
-        }
-        tmem_st16(sc + c * 16, p);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (masked) {
-        // Values that some row must not see: rows behind the keys (other sequences, padding) are
-        // zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows that
-        // see them at the end.  A thread goes over one key's row.
-        const int u = 2 * j + 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(kv_full(slot_of(u)), par_of(u), abort_flag));
-        if (!ok) break;
-        char* row = smem_raw + (ring - smem_u32(smem_raw)) + slot_of(u) * C::TILE + r * 128;
-        const bool gone = j * 128 + r >= pt.lk;
-#pragma unroll
-        for (int c = 0; c < C::CHUNKS; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4* p = reinterpret_cast<uint4*>(row + c * 16384 + ((i + r) & 7) * 16);
-            uint4 v = *p;
+          for (int c = 0; c < 128; ++c)
+            if (c >= lim) x[c] = 0xff800000u;  // -inf
+          // Values that some row must not see: rows behind the keys (other sequences, padding)
+          // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
+          // that see them at the end.  A thread goes over one key's row.
+          const int u = ub + 2 * jj + 1;
+          if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
+          char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
+          const bool gone = j * 128 + r >= item.lk;
+#pragma unroll 4
+          for (int k = 0; k < C::CHUNKS * 8; ++k) {
+            uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + ((k + r) & 7) * 16);
+            uint4 v = *q;
             if (gone) {
-              *p = make_uint4(0u, 0u, 0u, 0u);
+              *q = make_uint4(0u, 0u, 0u, 0u);
             } else {
               const bool b0 = drop_nonfinite(v.x), b1 = drop_nonfinite(v.y), b2 = drop_nonfinite(v.z),
                          b3 = drop_nonfinite(v.w);
               if (b0 || b1 || b2 || b3) {
-                *(volatile int*)&sb.poison = 1;
+                *(volatile int*)&sb.poison[it & 3] = it + 1;
                 __threadfence_block();  // a warp that finds the value gone finds the flag set
-                *p = v;
+                *q = v;
               }
             }
           }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        float mx4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx4[c] = max3_nan(__uint_as_float(x[c]), __uint_as_float(x[c + 4]), __uint_as_float(x[c + 8]));
+#pragma unroll
+        for (int c = 12; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx4[e] = max3_nan(mx4[e], __uint_as_float(x[c + e]), __uint_as_float(x[c + 4 + e]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx4[e] = max_nan(mx4[e], __uint_as_float(x[124 + e]));
+        const float mx = max_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3]);
+        const bool grow = mx > m + slack || mx != mx;
+        if (jj == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, grow)) {
+          const float f = grow ? ex2((m - mx) * sl) : 1.f;
+          if (grow) m = mx;
+          l *= f;
+          if (!(ok = wait(o_done(t), (ph - 1) & 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < HD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(oc + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(oc + c, o);
+          }
+        }
+        // nothing seen yet: every weight is 0; an infinite or NaN maximum makes the row NaN
+        float ms = m * sl;
+        if (!(fabsf(ms) < INFINITY)) ms = m == -INFINITY ? 0.f : NAN;
+        const uint64_t sl2 = pack2(sl, sl), ms2 = pack2(-ms, -ms);
+        uint64_t sum[2] = {0, 0};
+        if (!(ok = take_turn(jj))) break;
+        // A quarter's store is waited for after the next quarter's exponentials.  Masked scores are
+        // -inf, which exp2_fma does not take to 0.
+        auto weights = [&](auto fma) {
+#pragma unroll
+          for (int c = 0; c <= 4; ++c) {
+            if (c < 4) softmax_chunk<decltype(fma)::value>(x + c * 32, sl2, ms2, sum);
+            if (c == 3) pass_turn();
+            if (c > 0) {
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_full(t, c - 1));
+            }
+            if (c < 4) tmem_st16(sc + c * 16, x + c * 32);
+          }
+        };
+        if (masked)
+          weights(std::integral_constant<int, 0>());
+        else
+          weights(std::integral_constant<int, PROMPT_FMA>());
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full(t));
-    }
-    if (ok && nt[t] > 0) {
-      if (nb[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(o_done(t), (nb[t] - 1) & 1, abort_flag));
-      if (ok) {
-        tc_fence_after();
+      for (int k = nb; ok && k < sp.n; ++k) {
+        ok = take_turn(k);
+        pass_turn();
+      }
+      turns += sp.n;
+      if (!ok) break;
+      if (nt > 0 && (nb > 0 || a.splits == 1)) {
+        if (nb > 0) {
+          if (!(ok = wait(o_done(t), (done + nb - 1) & 1))) break;
+          tc_fence_after();
+        }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        __nv_bfloat16* o = (__nv_bfloat16*)a.o + (size_t)(pt.q0 + t0[t] + tl) * a.so +
-                           (size_t)(kh * group + r % group) * HD;
-        const bool poison = nb[t] > 0 && *(volatile int*)&sb.poison;
+        const size_t prow = (size_t)item.idx * 256 + t * 128 + r;  // row of the partial (splits > 1)
+        if (a.splits > 1) a.part_ml[prow] = make_float2(m * sl, l);
+        __nv_bfloat16* o = (__nv_bfloat16*)a.o + (size_t)(item.q0 + t0 + tl) * a.so +
+                           (size_t)(item.kh * group + r % group) * HD;
+        const bool poison = nb > 0 && *(volatile int*)&sb.poison[it & 3] == it + 1;
         // masked keys of either tile start here
-        const int from = max(0, (ctx + t0[0] + 1) & ~127);
+        const int from = max(max(0, (ctx + sp.t0[0] + 1) & ~127), sp.jb * 128);
+        const int to = min(ctx + t0 + nt, (sp.jb + nb) * 128);
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t x[32];
-          if (nb[t] > 0) {
+          if (nb > 0) {
             tmem_ld32(oc + c, x);
             tmem_wait_ld();
           } else {
@@ -299,9 +599,9 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
             for (int i = 0; i < 32; ++i) x[i] = 0;
           }
           if (poison) {
-            for (int key = from; key < ctx + t0[t] + nt[t]; ++key) {
+            for (int key = from; key < to; ++key) {
               const __nv_bfloat16* v =
-                  (const __nv_bfloat16*)a.v + (size_t)(pt.k0 + key) * a.sv + (size_t)kh * HD + c;
+                  (const __nv_bfloat16*)a.v + (size_t)(item.k0 + key) * a.sv + (size_t)item.kh * HD + c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float f = __bfloat162float(v[i]);
@@ -309,7 +609,12 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
               }
             }
           }
-          if (valid) {
+          if (a.splits > 1) {
+            float* dst = a.part + prow * HD + c;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          } else if (valid) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 w;
@@ -321,7 +626,10 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
             }
           }
         }
+        tc_fence_before();  // O is read before the next item's first product overwrites it
       }
+      done += nb;
+      ub += 2 * sp.n;
     }
   }
   tc_fence_before();
@@ -331,6 +639,50 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// Joins the key ranges of a pair of tiles: with M the largest maximum of a row's
+// partials, o = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, in range order.
+// One thread per four columns of a row; JOIN_ROWS rows of a pair per CTA.
+template <int HD>
+constexpr int prompt_join_rows() { return 256 / (HD / 4); }
+template <int HD>
+__global__ void __launch_bounds__(256) k_attn_prompt_join(PromptArgs a, int parts) {
+  pdl_wait();
+  constexpr int PER = HD / 4, ROWS = prompt_join_rows<HD>();
+  const int tok = 128 / a.group, pair = blockIdx.x / parts;
+  PromptTile pt;
+  if (!prompt_tile(a, pair / a.kv_heads, 2 * tok, pt)) return;
+  const int kh = pair % a.kv_heads;
+  const int row = (blockIdx.x % parts) * ROWS + (int)threadIdx.x / PER, c = ((int)threadIdx.x % PER) * 4;
+  const int t = row >> 7, r = row & 127, token = (pt.tile * 2 + t) * tok + r / a.group;
+  if ((int)threadIdx.x >= ROWS * PER || row >= 256 || r >= tok * a.group || token >= pt.lq) return;
+  const PromptItem it = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, kh, 0, 0};
+  const PromptSpan whole(it, tok, 1);
+  const int blocks = t ? whole.nb[1] : whole.nb[0];
+  const int n = blocks ? cdiv(blocks, cdiv(whole.n, a.splits)) : 0;  // ranges with keys
+  const size_t p0 = (size_t)pair * a.splits * 256 + row;
+  float M = -INFINITY;
+  for (int s = 0; s < n; ++s) M = max_nan(M, a.part_ml[p0 + (size_t)s * 256].x);
+  const float ms = M == -INFINITY ? 0.f : M;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const size_t p = p0 + (size_t)s * 256;
+    const float2 ml = a.part_ml[p];
+    const float w = ex2(ml.x - ms);
+    const float4 v = *reinterpret_cast<const float4*>(a.part + p * HD + c);
+    l += w * ml.y;
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (size_t)(pt.q0 + token) * a.so +
+                            (size_t)(kh * a.group + r % a.group) * HD + c) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
 }
 
 template <int HD>
@@ -349,13 +701,26 @@ static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(k_attn_prompt_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) !=
+    if (cudaFuncSetAttribute(k_attn_prompt_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prompt_smem<HD>()) !=
         cudaSuccess)
       return LT_ERR_CUDA;
     if (dev >= 0 && dev < 64) set[dev] = true;
   }
-  const unsigned tiles = (unsigned)(a.n_q / (C::NT * tok) + a.n_seqs);
-  k_attn_prompt_tc<HD><<<tiles * a.kv_heads, C::THREADS, C::SMEM, st>>>(a, mq, mk, mv);
+  const unsigned pairs = (unsigned)prompt_pairs(a.n_q, a.n_seqs, a.group) * a.kv_heads;
+  k_attn_prompt_tc<HD><<<pairs * a.splits, C::THREADS, prompt_smem<HD>(), st>>>(a, mq, mk, mv);
+  if (a.splits > 1) {
+    cudaLaunchConfig_t cfg = {};
+    const int parts = cdiv(256, prompt_join_rows<HD>());
+    cfg.gridDim = dim3(pairs * parts);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_attn_prompt_join<HD>, a, parts) != cudaSuccess) return LT_ERR_CUDA;
+  }
   return cudaGetLastError() == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 

@@ -73,10 +73,16 @@ extern "C" int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int 
                                             int head_dim, size_t* bytes) {
   if (!bytes || (dtype != LT_F32 && dtype != LT_BF16) || n_q < 0 || n_seqs < 0) return LT_ERR_ARG;
   if (!attn_shape_ok(n_heads, n_kv_heads, head_dim)) return LT_ERR_SHAPE;
-  // the launch grid counts tiles of 64 / group tokens
+  // the launch grid counts tiles of at least 64 / group tokens
   if (((long long)n_q / (SIMT_M / (n_heads / n_kv_heads)) + n_seqs) * n_kv_heads > 0x7fffffff)
     return LT_ERR_SHAPE;
   *bytes = 256;
+  if (dtype == LT_BF16) {
+    const long long splits = prompt_splits(n_q, n_seqs, n_heads, n_kv_heads);
+    if (splits > 1)
+      *bytes = (size_t)(prompt_pairs(n_q, n_seqs, n_heads / n_kv_heads) * n_kv_heads * splits) * 256 *
+               (sizeof(float2) + (size_t)head_dim * sizeof(float));
+  }
   return LT_OK;
 }
 
@@ -95,13 +101,19 @@ extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, co
   if (!d_q || !d_o || !d_q_off || !d_scratch || (n_kv > 0 && (!d_k || !d_v))) return LT_ERR_ARG;
   const long long w = (long long)n_heads * head_dim, wk = (long long)n_kv_heads * head_dim;
   if (stride_q < w || stride_o < w || stride_k < wk || stride_v < wk) return LT_ERR_ARG;
-  if (!attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_k, stride_k) ||
+  if (((uintptr_t)d_scratch & 15) || !attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_k, stride_k) ||
       !attn_aligned(dtype, d_v, stride_v) || !attn_aligned(dtype, d_o, stride_o))
     return LT_ERR_SHAPE;
   if (scratch_bytes < need) return LT_ERR_CAPACITY;
   PromptArgs a = {d_q, d_k, d_v, d_o, stride_q, stride_k, stride_v, stride_o, d_q_off,
                   d_kv_off ? d_kv_off : d_q_off, n_seqs, n_q, n_kv, n_heads, n_kv_heads,
-                  n_heads / n_kv_heads, scale, d_status};
+                  n_heads / n_kv_heads, scale, d_status, 1, nullptr, nullptr};
+  if (dtype == LT_BF16) {
+    a.splits = prompt_splits(n_q, n_seqs, n_heads, n_kv_heads);
+    const size_t slots = (size_t)(prompt_pairs(n_q, n_seqs, a.group) * n_kv_heads * a.splits) * 256;
+    a.part = (float*)d_scratch;
+    a.part_ml = (float2*)(a.part + slots * head_dim);
+  }
   cudaStream_t st = (cudaStream_t)stream;
   switch (head_dim) {
     case 32: return prompt_any<32>(dtype, a, st);

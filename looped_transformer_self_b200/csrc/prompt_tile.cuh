@@ -17,6 +17,9 @@ struct PromptArgs {
   int n_seqs, n_q, n_kv, heads, kv_heads, group;
   float scale;
   int* status;
+  int splits;        // key ranges of a pair of tiles, each an item of its own (bf16)
+  float2* part_ml;   // partials of the ranges: [pairs * splits][256] maximum (log2 units) and sum
+  float* part;       // [pairs * splits][256][head_dim] unnormalised outputs
 };
 
 // Tile `t` of the packed batch in units of `tok` tokens: its sequence and its
@@ -53,6 +56,18 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int t, int tok,
     t -= __shfl_sync(0xffffffffu, incl, 31);
   }
   return false;
+}
+
+// Pairs of 128-row tiles per key/value head, at most.
+inline long long prompt_pairs(int n_q, int n_seqs, int group) { return n_q / (2 * (128 / group)) + (long long)n_seqs; }
+
+// Key ranges: when the pairs leave SMs without work, each pair's keys are cut
+// so that there is an item for every SM.  One range otherwise: partials cost a
+// write, a read and a launch.
+inline int prompt_splits(int n_q, int n_seqs, int heads, int kv_heads) {
+  const long long pairs = prompt_pairs(n_q, n_seqs, heads / kv_heads) * kv_heads;
+  const int sms = attn_sm_count();
+  return pairs >= sms ? 1 : (int)((sms + pairs - 1) / (pairs > 0 ? pairs : 1));
 }
 
 }  // namespace lt

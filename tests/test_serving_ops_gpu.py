@@ -421,7 +421,8 @@ def test_captured_graphs_follow_new_lengths_and_share_the_card():
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
             res = step()
-        outs.append((g, s, q, k, v, cache, qo, ro, po, pre, to, o1, o2, res, (p, dq, x, ua, ud), (sc1, sc2)))
+        # the graph reads every tensor of the calls, the offsets vo among them
+        outs.append((g, s, q, k, v, cache, qo, ro, po, pre, to, o1, o2, res, (p, dq, x, ua, ud), (sc1, sc2, vo)))
     for lens, rows, np_ in (([cap], 4, 100), ([17, 300], 9, 399), ([1], 1, 0)):
         for g, s, q, k, v, cache, qo, ro, po, pre, to, o1, o2, res, ver, _ in outs:
             qo.copy_(torch.tensor([0, sum(lens)], dtype=torch.int32))
