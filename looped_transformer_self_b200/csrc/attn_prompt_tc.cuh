@@ -22,8 +22,6 @@
 // item run under the softmax and output of the last.
 #pragma once
 
-#include <type_traits>
-
 #include "attn_tc.cuh"
 #include "prompt_tile.cuh"
 
@@ -78,10 +76,7 @@ struct PromptSpan {
   }
 };
 
-// 2^y for y <= 0 on the FMA pipe, two at a time: y = n + f with n the nearest
-// integer (taken by adding and subtracting 1.5 * 2^23), 2^f = 1 + f g(f) with g
-// of degree 4 fitted to the least relative error on [-1/2, 1/2] (2^-22.3 in
-// fp32), and n added to the exponent.  y below -126 counts as -126.
+// Two fp32 operations per instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -100,44 +95,15 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ void exp2_fma(uint64_t y, float& e0, float& e1) {
-  float a, b;
-  unpack2(y, a, b);
-  y = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
-  const uint64_t big = pack2(12582912.f, 12582912.f), nbig = pack2(-12582912.f, -12582912.f);
-  const uint64_t t = add2(y, big);
-  const uint64_t nt = add2(t, nbig);
-  const uint64_t f = fma2(nt, pack2(-1.f, -1.f), y);
-  uint64_t p = fma2(pack2(0.001326472731307149f, 0.001326472731307149f), f,
-                    pack2(0.009671512991189957f, 0.009671512991189957f));
-  p = fma2(p, f, pack2(0.05550733581185341f, 0.05550733581185341f));
-  p = fma2(p, f, pack2(0.24022242426872253f, 0.24022242426872253f));
-  p = fma2(p, f, pack2(0.6931470036506653f, 0.6931470036506653f));
-  p = fma2(p, f, pack2(1.f, 1.f));
-  float p0, p1, t0, t1;
-  unpack2(p, p0, p1);
-  unpack2(t, t0, t1);
-  e0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  e1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
 // 32 scores x of a row to weights 2^(x sl + nms), as bf16 pairs in the first half
-// of x, and their fp32 values added to `sum`; FMA of every eight pairs on the FMA pipe.
-#ifndef PROMPT_FMA
-#define PROMPT_FMA 2
-#endif
-template <int FMA>
+// of x, and their fp32 values added to `sum`.
 __device__ __forceinline__ void softmax_chunk(uint32_t* x, uint64_t sl2, uint64_t nms2, uint64_t* sum) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint64_t y = fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl2, nms2);
     float e0, e1;
-    if (i % 8 < FMA) {
-      exp2_fma(y, e0, e1);
-    } else {
-      unpack2(y, e0, e1);
-      e0 = ex2(e0);
-      e1 = ex2(e1);
-    }
+    unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl2, nms2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
     sum[i & 1] = add2(sum[i & 1], pack2(e0, e1));
     x[i] = pack_bf16(e0, e1);
   }
@@ -348,8 +314,9 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
               if (!(ok = ok && wait(p_full(t, c), par))) break;
               tc_fence_after();
               if (elect_one()) {
-                tc_mma_ts(ot, st + c * 16, v + c * 256, IO, j > 1 || c > 0);
-                tc_mma_ts(ot, st + c * 16 + 8, v + c * 256 + 128, IO, 1);
+#pragma unroll
+                for (int i = 2 * c; i < 2 * c + 2; ++i)
+                  tc_mma_ts(ot, st + i * 8, v + i * 128, IO, j > 1 || i > 0);
                 if (c == 3) tc_commit(o_bar);
               }
               __syncwarp();
@@ -478,10 +445,14 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         tmem_wait_ld();
         const bool masked = (j + 1) * 128 > see_first;
         if (masked) {
-          const int lim = see - j * 128;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c >= lim) x[c] = 0xff800000u;  // -inf
+          for (int c = 0; c < 4; ++c) {
+            const int lim = min(max(see - j * 128 - c * 32, 0), 32);
+            const uint32_t hide = lim == 32 ? 0u : 0xffffffffu << lim;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (hide & (1u << i)) x[c * 32 + i] = 0xff800000u;  // -inf
+          }
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
           // that see them at the end.  A thread goes over one key's row.
@@ -489,23 +460,30 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
           char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
           const bool gone = j * 128 + r >= item.lk;
-#pragma unroll 4
+          uint32_t bad = 0;
+#pragma unroll
           for (int k = 0; k < C::CHUNKS * 8; ++k) {
-            uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + ((k + r) & 7) * 16);
-            uint4 v = *q;
-            if (gone) {
-              *q = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-              const bool b0 = drop_nonfinite(v.x), b1 = drop_nonfinite(v.y), b2 = drop_nonfinite(v.z),
-                         b3 = drop_nonfinite(v.w);
-              if (b0 || b1 || b2 || b3) {
-                *(volatile int*)&sb.poison[it & 3] = it + 1;
-                __threadfence_block();  // a warp that finds the value gone finds the flag set
-                *q = v;
-              }
-            }
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * 16384 + ((k + r) & 7) * 16);
+            bad |= nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) | nonfinite_bits(v.w);
           }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (gone || bad) {
+            if (!gone) {
+              *(volatile int*)&sb.poison[it & 3] = it + 1;
+              __threadfence_block();  // a warp that finds the value gone finds the flag set
+            }
+#pragma unroll 1
+            for (int k = 0; k < C::CHUNKS * 8; ++k) {
+              uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + (k & 7) * 16);
+              uint4 v = *q;
+              if (gone) v = make_uint4(0u, 0u, 0u, 0u);
+              drop_nonfinite(v.x);
+              drop_nonfinite(v.y);
+              drop_nonfinite(v.z);
+              drop_nonfinite(v.w);
+              *q = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
         }
         float mx4[4];
 #pragma unroll
@@ -544,26 +522,19 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         const uint64_t sl2 = pack2(sl, sl), ms2 = pack2(-ms, -ms);
         uint64_t sum[2] = {0, 0};
         if (!(ok = take_turn(jj))) break;
-        // A quarter's store is waited for after the next quarter's exponentials.  Masked scores are
-        // -inf, which exp2_fma does not take to 0.
-        auto weights = [&](auto fma) {
+        // a quarter's store is waited for after the next quarter's exponentials
 #pragma unroll
-          for (int c = 0; c <= 4; ++c) {
-            if (c < 4) softmax_chunk<decltype(fma)::value>(x + c * 32, sl2, ms2, sum);
-            if (c == 3) pass_turn();
-            if (c > 0) {
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(p_full(t, c - 1));
-            }
-            if (c < 4) tmem_st16(sc + c * 16, x + c * 32);
+        for (int c = 0; c <= 4; ++c) {
+          if (c < 4) softmax_chunk(x + c * 32, sl2, ms2, sum);
+          if (c == 3) pass_turn();
+          if (c > 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(t, c - 1));
           }
-        };
-        if (masked)
-          weights(std::integral_constant<int, 0>());
-        else
-          weights(std::integral_constant<int, PROMPT_FMA>());
+          if (c < 4) tmem_st16(sc + c * 16, x + c * 32);
+        }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
@@ -612,17 +583,18 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           if (a.splits > 1) {
             float* dst = a.part + prow * HD + c;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(dst + 4 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) st_global32(dst + 8 * i, x + 8 * i);
           } else if (valid) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(x[8 * i]) * inv, __uint_as_float(x[8 * i + 1]) * inv);
-              w.y = pack_bf16(__uint_as_float(x[8 * i + 2]) * inv, __uint_as_float(x[8 * i + 3]) * inv);
-              w.z = pack_bf16(__uint_as_float(x[8 * i + 4]) * inv, __uint_as_float(x[8 * i + 5]) * inv);
-              w.w = pack_bf16(__uint_as_float(x[8 * i + 6]) * inv, __uint_as_float(x[8 * i + 7]) * inv);
-              *reinterpret_cast<uint4*>(o + c + 8 * i) = w;
+            for (int i = 0; i < 16; ++i)
+              x[i] = pack_bf16(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+            if (a.o_wide) {  // a row's 64 bytes in two stores of whole 32-byte sectors
+              st_global32(o + c, x);
+              st_global32(o + c + 16, x + 8);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(o + c + 8 * i) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
             }
           }
         }

@@ -93,6 +93,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// Nonzero if either half of a bf16 pair is infinite or NaN: an exponent of all
+// ones carries into the half's sign bit.
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t x) {
+  return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+}
+// 32 bytes to a 32-byte aligned address in one store.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Zeroes the halves of a bf16 pair that are infinite or NaN; true if there were any.
 __device__ __forceinline__ bool drop_nonfinite(uint32_t& x) {
   const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;

@@ -101,13 +101,14 @@ extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, co
   if (!d_q || !d_o || !d_q_off || !d_scratch || (n_kv > 0 && (!d_k || !d_v))) return LT_ERR_ARG;
   const long long w = (long long)n_heads * head_dim, wk = (long long)n_kv_heads * head_dim;
   if (stride_q < w || stride_o < w || stride_k < wk || stride_v < wk) return LT_ERR_ARG;
-  if (((uintptr_t)d_scratch & 15) || !attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_k, stride_k) ||
+  if (((uintptr_t)d_scratch & 31) || !attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_k, stride_k) ||
       !attn_aligned(dtype, d_v, stride_v) || !attn_aligned(dtype, d_o, stride_o))
     return LT_ERR_SHAPE;
   if (scratch_bytes < need) return LT_ERR_CAPACITY;
   PromptArgs a = {d_q, d_k, d_v, d_o, stride_q, stride_k, stride_v, stride_o, d_q_off,
                   d_kv_off ? d_kv_off : d_q_off, n_seqs, n_q, n_kv, n_heads, n_kv_heads,
-                  n_heads / n_kv_heads, scale, d_status, 1, nullptr, nullptr};
+                  n_heads / n_kv_heads, scale, d_status, 1, nullptr,
+                  ((uintptr_t)d_o & 31) == 0 && stride_o % 16 == 0, nullptr};
   if (dtype == LT_BF16) {
     a.splits = prompt_splits(n_q, n_seqs, n_heads, n_kv_heads);
     const size_t slots = (size_t)(prompt_pairs(n_q, n_seqs, a.group) * n_kv_heads * a.splits) * 256;

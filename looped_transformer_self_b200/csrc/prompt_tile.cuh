@@ -19,6 +19,7 @@ struct PromptArgs {
   int* status;
   int splits;        // key ranges of a pair of tiles, each an item of its own (bf16)
   float2* part_ml;   // partials of the ranges: [pairs * splits][256] maximum (log2 units) and sum
+  int o_wide;        // output rows start on 32-byte boundaries
   float* part;       // [pairs * splits][256][head_dim] unnormalised outputs
 };
 
