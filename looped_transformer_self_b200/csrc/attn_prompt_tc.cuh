@@ -57,9 +57,12 @@ struct PromptSmem {
 template <int HD>
 constexpr size_t prompt_smem() { return PromptTc<HD>::TILES + sizeof(PromptSmem); }
 
-// What an item covers: per tile first token, tokens, key blocks of its range.
+// What an item covers: per tile first token, tokens and blocks, and the ring's
+// blocks jb .. jb + n - 1.  The tiles share every block (step 1), except that an
+// item of a cut pair whose second tile is empty gives its rows to both, which
+// take the blocks in turn (step 2) and leave a partial each.
 struct PromptSpan {
-  int t0[2], nt[2], nb[2], n, jb;
+  int t0[2], nt[2], nb[2], n, jb, step;
   __device__ __forceinline__ PromptSpan(const PromptItem& it, int tok, int splits) {
     int full[2];
 #pragma unroll
@@ -73,7 +76,17 @@ struct PromptSpan {
 #pragma unroll
     for (int i = 0; i < 2; ++i) nb[i] = max(0, min(full[i] - jb, chunk));
     n = max(nb[0], nb[1]);
+    step = 1;
+    if (splits > 1 && nt[1] == 0) {
+      step = 2;
+      t0[1] = t0[0];
+      nt[1] = nt[0];
+      nb[1] = n >> 1;
+      nb[0] = n - nb[1];
+    }
   }
+  // ring block of the tile's k-th block, from jb
+  __device__ __forceinline__ int at(int t, int k) const { return step == 2 ? 2 * k + t : k; }
 };
 
 // Two fp32 operations per instruction.
@@ -165,6 +178,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.group, tok = 128 / group;
+  pdl_trigger();  // the join may be launched: it waits for this grid's end before it reads
 
   const uint32_t q_s = smem_u32(smem_raw), ring = q_s + 2 * C::TILE;
   const uint32_t q_full = smem_u32(&sb.q_full), q_empty = smem_u32(&sb.q_empty), fin = smem_u32(&sb.fin);
@@ -300,15 +314,15 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         ++qn;
         // Step j: the product of block j - 1's weights, then S of block j.  A slot is given back by
         // both tiles, used or not, and not before it is full: no tile gets a turn of the ring ahead.
-        int v_slot = 0;
+        int v_slot = 0, s_next = 0, p_next = 0;  // blocks whose S is out; the one whose product follows, + 1
         uint32_t v_par = 0;
         for (int j = 0; j <= sp.n; ++j) {
           const int k_slot = slot;
           const uint32_t k_par = ring_par;
           if (j > 0 && !(ok = wait(kv_full(v_slot), v_par))) break;
-          if (j > 0 && j <= nb) {
+          if (p_next > 0) {
             const uint64_t v = dv + (uint32_t)(v_slot * (C::TILE >> 4));
-            const uint32_t par = (uint32_t)(done + j - 1) & 1;
+            const uint32_t par = (uint32_t)(done + p_next - 1) & 1;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (!(ok = ok && wait(p_full(t, c), par))) break;
@@ -316,16 +330,18 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
               if (elect_one()) {
 #pragma unroll
                 for (int i = 2 * c; i < 2 * c + 2; ++i)
-                  tc_mma_ts(ot, st + i * 8, v + i * 128, IO, j > 1 || i > 0);
+                  tc_mma_ts(ot, st + i * 8, v + i * 128, IO, p_next > 1 || i > 0);
                 if (c == 3) tc_commit(o_bar);
               }
               __syncwarp();
             }
             if (!ok) break;
+            p_next = 0;
           }
           if (j < sp.n) {
             if (!(ok = wait(kv_full(k_slot), k_par))) break;
-            if (j < nb) {
+            if (s_next < nb && j == sp.at(t, s_next)) {
+              p_next = ++s_next;
               tc_fence_after();
               const uint64_t k = dk + (uint32_t)(k_slot * (C::TILE >> 4));
               if (elect_one()) {
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
       const int see_first = ctx + t0 + 1;             // keys the tile's first row sees
       float m = -INFINITY, l = 0.f;                   // m: reference maximum of the raw scores
       for (int jj = 0; jj < nb; ++jj) {
-        const int j = sp.jb + jj, ph = done + jj;
+        const int jr = sp.at(t, jj), j = sp.jb + jr, ph = done + jj;
         if (!(ok = wait(s_full(t), ph & 1))) break;
         tc_fence_after();
         uint32_t x[128];
@@ -456,7 +472,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
           // that see them at the end.  A thread goes over one key's row.
-          const int u = ub + 2 * jj + 1;
+          const int u = ub + 2 * jr + 1;
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
           char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
           const bool gone = j * 128 + r >= item.lk;
@@ -539,11 +555,12 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
-      for (int k = nb; ok && k < sp.n; ++k) {
+      const int most = max(sp.nb[0], sp.nb[1]);
+      for (int k = nb; ok && k < most; ++k) {
         ok = take_turn(k);
         pass_turn();
       }
-      turns += sp.n;
+      turns += most;
       if (!ok) break;
       if (nt > 0 && (nb > 0 || a.splits == 1)) {
         if (nb > 0) {
@@ -552,13 +569,13 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t prow = (size_t)item.idx * 256 + t * 128 + r;  // row of the partial (splits > 1)
-        if (a.splits > 1) a.part_ml[prow] = make_float2(m * sl, l);
+        if (a.splits > 1 && valid) a.part_ml[prow] = make_float2(m * sl, l);
         __nv_bfloat16* o = (__nv_bfloat16*)a.o + (size_t)(item.q0 + t0 + tl) * a.so +
                            (size_t)(item.kh * group + r % group) * HD;
         const bool poison = nb > 0 && *(volatile int*)&sb.poison[it & 3] == it + 1;
         // masked keys of either tile start here
         const int from = max(max(0, (ctx + sp.t0[0] + 1) & ~127), sp.jb * 128);
-        const int to = min(ctx + t0 + nt, (sp.jb + nb) * 128);
+        const int to = min(ctx + t0 + nt, (sp.jb + sp.n) * 128);
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t x[32];
@@ -571,6 +588,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           }
           if (poison) {
             for (int key = from; key < to; ++key) {
+              if (sp.step == 2 && (((key >> 7) - sp.jb) & 1) != t) continue;  // the other tile's
               const __nv_bfloat16* v =
                   (const __nv_bfloat16*)a.v + (size_t)(item.k0 + key) * a.sv + (size_t)item.kh * HD + c;
 #pragma unroll
@@ -580,11 +598,12 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
               }
             }
           }
+          if (!valid) continue;
           if (a.splits > 1) {
             float* dst = a.part + prow * HD + c;
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_global32(dst + 8 * i, x + 8 * i);
-          } else if (valid) {
+          } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               x[i] = pack_bf16(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
@@ -631,25 +650,43 @@ __global__ void __launch_bounds__(256) k_attn_prompt_join(PromptArgs a, int part
   if ((int)threadIdx.x >= ROWS * PER || row >= 256 || r >= tok * a.group || token >= pt.lq) return;
   const PromptItem it = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, kh, 0, 0};
   const PromptSpan whole(it, tok, 1);
-  const int blocks = t ? whole.nb[1] : whole.nb[0];
-  const int n = blocks ? cdiv(blocks, cdiv(whole.n, a.splits)) : 0;  // ranges with keys
+  const int blocks = t ? whole.nb[1] : whole.nb[0], chunk = cdiv(whole.n, a.splits);
+  // a range's partial, or its two where both tiles took the rows (blocks in turn)
+  const int two = whole.nt[1] == 0 ? 2 : 1;
   const size_t p0 = (size_t)pair * a.splits * 256 + row;
-  float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = max_nan(M, a.part_ml[p0 + (size_t)s * 256].x);
-  const float ms = M == -INFINITY ? 0.f : M;
-  float l = 0.f;
+  float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const size_t p = p0 + (size_t)s * 256;
-    const float2 ml = a.part_ml[p];
-    const float w = ex2(ml.x - ms);
-    const float4 v = *reinterpret_cast<const float4*>(a.part + p * HD + c);
-    l += w * ml.y;
-    o.x = fmaf(w, v.x, o.x);
-    o.y = fmaf(w, v.y, o.y);
-    o.z = fmaf(w, v.z, o.z);
-    o.w = fmaf(w, v.w, o.w);
+  constexpr int B = 8;  // partials in flight
+  for (int k0 = 0; (k0 / two) * chunk < blocks; k0 += B) {
+    float2 ml[B];
+    float4 v[B];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const int s = (k0 + i) / two, e = (k0 + i) % two;
+      const bool there = s * chunk + e < blocks && e < chunk;
+      const size_t p = p0 + (size_t)s * 256 + e * 128;
+      ml[i] = there ? a.part_ml[p] : make_float2(-INFINITY, 0.f);
+      v[i] = there ? *reinterpret_cast<const float4*>(a.part + p * HD + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mx = M;
+#pragma unroll
+    for (int i = 0; i < B; ++i) mx = max_nan(mx, ml[i].x);
+    const float ms = mx == -INFINITY ? 0.f : mx, f = ex2(M - ms);
+    M = mx;
+    l *= f;
+    o.x *= f;
+    o.y *= f;
+    o.z *= f;
+    o.w *= f;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const float w = ex2(ml[i].x - ms);
+      l += w * ml[i].y;
+      o.x = fmaf(w, v[i].x, o.x);
+      o.y = fmaf(w, v[i].y, o.y);
+      o.z = fmaf(w, v[i].z, o.z);
+      o.w = fmaf(w, v[i].w, o.w);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (size_t)(pt.q0 + token) * a.so +

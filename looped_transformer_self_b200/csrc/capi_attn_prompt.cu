@@ -78,7 +78,7 @@ extern "C" int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int 
     return LT_ERR_SHAPE;
   *bytes = 256;
   if (dtype == LT_BF16) {
-    const long long splits = prompt_splits(n_q, n_seqs, n_heads, n_kv_heads);
+    const long long splits = prompt_max_splits(n_q, n_seqs, n_heads, n_kv_heads);
     if (splits > 1)
       *bytes = (size_t)(prompt_pairs(n_q, n_seqs, n_heads / n_kv_heads) * n_kv_heads * splits) * 256 *
                (sizeof(float2) + (size_t)head_dim * sizeof(float));
@@ -110,7 +110,7 @@ extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, co
                   n_heads / n_kv_heads, scale, d_status, 1, nullptr,
                   ((uintptr_t)d_o & 31) == 0 && stride_o % 16 == 0, nullptr};
   if (dtype == LT_BF16) {
-    a.splits = prompt_splits(n_q, n_seqs, n_heads, n_kv_heads);
+    a.splits = prompt_splits(n_q, n_kv, n_seqs, n_heads, n_kv_heads);
     const size_t slots = (size_t)(prompt_pairs(n_q, n_seqs, a.group) * n_kv_heads * a.splits) * 256;
     a.part = (float*)d_scratch;
     a.part_ml = (float2*)(a.part + slots * head_dim);

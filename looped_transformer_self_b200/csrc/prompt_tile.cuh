@@ -62,13 +62,20 @@ __device__ __forceinline__ bool prompt_tile(const PromptArgs& a, int t, int tok,
 // Pairs of 128-row tiles per key/value head, at most.
 inline long long prompt_pairs(int n_q, int n_seqs, int group) { return n_q / (2 * (128 / group)) + (long long)n_seqs; }
 
-// Key ranges: when the pairs leave SMs without work, each pair's keys are cut
-// so that there is an item for every SM.  One range otherwise: partials cost a
-// write, a read and a launch.
-inline int prompt_splits(int n_q, int n_seqs, int heads, int kv_heads) {
+// Key ranges of a pair of tiles, at most: an item for every SM.
+inline int prompt_max_splits(int n_q, int n_seqs, int heads, int kv_heads) {
   const long long pairs = prompt_pairs(n_q, n_seqs, heads / kv_heads) * kv_heads;
   const int sms = attn_sm_count();
-  return pairs >= sms ? 1 : (int)((sms + pairs - 1) / (pairs > 0 ? pairs : 1));
+  return pairs <= 0 || pairs * 2 > sms ? 1 : (int)(sms / pairs);
+}
+// Key ranges taken: partials cost a write, a read and a second kernel (6 us for
+// 48 pairs of 5 blocks, 16.6 us whole), a block about 1.6 us, so a range keeps
+// at least 6 blocks of an average sequence's keys (32 pairs of up to 47 blocks:
+// 80 us whole, 37 us in 4 ranges).
+inline int prompt_splits(int n_q, int n_kv, int n_seqs, int heads, int kv_heads) {
+  const long long blocks = (long long)n_kv / (n_seqs > 0 ? n_seqs : 1) / 128;
+  const long long most = prompt_max_splits(n_q, n_seqs, heads, kv_heads);
+  return (int)(blocks / 6 < 1 ? 1 : blocks / 6 < most ? blocks / 6 : most);
 }
 
 }  // namespace lt
