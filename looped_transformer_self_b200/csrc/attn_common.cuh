@@ -193,6 +193,10 @@ inline bool attn_shape_ok(int n_heads, int n_kv_heads, int head_dim) {
   return n_kv_heads > 0 && n_kv_heads <= 1024 && n_heads > 0 && n_heads % n_kv_heads == 0 &&
          n_heads / n_kv_heads <= ATTN_MAX_GROUP;
 }
+// Lets a kernel take `bytes` of dynamic shared memory (the attribute belongs to a device).
+inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
 // Rows start on 16-byte boundaries (vector loads and TMA).
 inline bool attn_aligned(int dtype, const void* p, long long stride) {
   return ((uintptr_t)p & 15) == 0 && (stride * (dtype == 0 ? 4 : 2)) % 16 == 0;

@@ -2,7 +2,7 @@
 //
 // A tile is (group of rows, key/value head, up to MT packed query rows); its
 // keys are the group's prefix slots followed by the tail slots of the tile's
-// own rows, in blocks of PREFIX_N.  The (tile, block) units of all tiles are
+// own rows, in blocks of BN.  The (tile, block) units of all tiles are
 // laid end to end and CTA c of n takes units [c U / n, (c + 1) U / n),
 // so every CTA streams the same number of blocks whatever the lengths are.
 // Lengths are read on the device: a captured call follows them.
@@ -16,7 +16,6 @@
 
 namespace lt {
 
-constexpr int PREFIX_N = 64;
 
 struct PrefixArgs {
   const void* q;
@@ -33,8 +32,8 @@ struct PrefixArgs {
   // scratch
   long long* head;  // [0]: U
   int4* tile_tab;   // per tile: first unit (x low, y high), blocks, 0
-  int4* row_tab;    // per row: tile of key/value head 0, tiles per head, first packed row, 0
-  float2* ml;       // [slots][MT]: running maximum (log2 units of its kernel) and sum
+  int4* row_tab;    // per row: tile of key/value head 0, tiles per head, first packed row, partials of a part
+  float2* part_ml;  // [slots][MT]: maximum (log2 units) and sum
   float* part;      // [slots][MT][hd] unnormalised outputs
   int max_tiles;
   int* status;
@@ -54,14 +53,18 @@ __device__ __forceinline__ int2 prefix_tail(const PrefixArgs& a, int row, int n)
   const int y = off_range(a.tail_off, row + n - 1, a.n_tail, a.status).y;
   return {x, max(x, y)};
 }
-__device__ __forceinline__ int prefix_blocks(int np, int nt) { return max(1, cdiv(np + nt, PREFIX_N)); }
+template <int BN>
+__device__ __forceinline__ int prefix_blocks(int np, int nt) {
+  return max(1, cdiv(np + nt, BN));
+}
 
 // Blocks of all row tiles of one group (one key/value head).
+template <int BN>
 __device__ __forceinline__ int prefix_group_blocks(const PrefixArgs& a, const PrefixGroup& g, int tok) {
   int n = 0;
   for (int i = 0; i < g.m; i += tok) {
     const int2 t = prefix_tail(a, g.r0 + i, min(tok, g.m - i));
-    n += prefix_blocks(g.np, t.y - t.x);
+    n += prefix_blocks<BN>(g.np, t.y - t.x);
   }
   return n;
 }
@@ -77,18 +80,20 @@ __device__ __forceinline__ long long warp_incl_scan(long long v) {
 }
 
 // Units of all groups (every warp computes it alike).
+template <int BN>
 __device__ __forceinline__ long long prefix_total(const PrefixArgs& a, int tok) {
   const int lane = threadIdx.x & 31;
   long long n = 0;
   for (int g = lane; g < a.n_groups; g += 32) {
     const PrefixGroup pg = prefix_group(a, g);
-    n += (long long)a.kv_heads * prefix_group_blocks(a, pg, tok);
+    n += (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   return n;
 }
 
+template <int BN>
 struct PrefixPos {
   PrefixGroup g;
   int gi, kh, mt, nmt;   // group, key/value head, row tile, row tiles of the group
@@ -101,7 +106,7 @@ struct PrefixPos {
     row0 = g.r0 + mt * tok;
     nrow = min(tok, g.m - mt * tok);
     tail = prefix_tail(a, row0, nrow);
-    nb = prefix_blocks(g.np, tail.y - tail.x);
+    nb = prefix_blocks<BN>(g.np, tail.y - tail.x);
   }
   // The tile that holds unit u (u below the total).
   __device__ __forceinline__ void find(const PrefixArgs& a, int tok, long long u) {
@@ -113,7 +118,7 @@ struct PrefixPos {
       int blocks = 0;
       if (s0 + lane < a.n_groups) {
         pg = prefix_group(a, s0 + lane);
-        blocks = prefix_group_blocks(a, pg, tok);
+        blocks = prefix_group_blocks<BN>(a, pg, tok);
         units = (long long)a.kv_heads * blocks;
         nt = (long long)a.kv_heads * cdiv(pg.m, tok);
       }
@@ -164,13 +169,17 @@ struct PrefixPos {
     }
     set_tile(a, tok);
   }
-  // Entries of the tables that the merge reads, written by the CTA with the tile's first block.
-  __device__ __forceinline__ void publish(const PrefixArgs& a, int tok) const {
-    if (threadIdx.x == 0)
+  // Entries of the tables that the merge reads, written by the CTA with the tile's first block
+  // (threads `id` of n; `half`: rows of a 128-row half of the tile, 0 for tiles in one piece;
+  // `two`: a part of more than one block has two partials, see TcSpan).
+  __device__ __forceinline__ void publish(const PrefixArgs& a, int id, int n, int half = 0, bool two = false) const {
+    if (id == 0)
       a.tile_tab[t] = make_int4((int)(unsigned)(u0 & 0xffffffffll), (int)(u0 >> 32), nb, 0);
     if (kh == 0)
-      for (int i = threadIdx.x; i < nrow; i += blockDim.x)
-        a.row_tab[row0 + i] = make_int4(t, nmt, i * a.group, 0);
+      for (int i = id; i < nrow; i += n) {
+        const int r = half ? i / half * 128 + i % half * a.group : i * a.group;
+        a.row_tab[row0 + i] = make_int4(t, nmt, r, two ? 2 : 1);
+      }
   }
 };
 

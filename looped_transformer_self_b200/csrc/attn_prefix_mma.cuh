@@ -9,10 +9,11 @@
 // rows' pieces of one column lie in different banks (ldmatrix).
 #pragma once
 
-#include "attn_prefix.cuh"
-#include "attn_tc.cuh"
+#include "attn_tc_kernel.cuh"
 
 namespace lt {
+
+constexpr int PREFIX_N = 64;  // keys of a block
 
 template <int HD, int MT>
 struct PrefixMma {
@@ -27,9 +28,6 @@ struct PrefixMma {
   static_assert((size_t)WARPS * 16 * (HD + 4) * 4 <= SMEM, "the merge reuses the ring");
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -61,21 +59,21 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
   const int gr = lane >> 2, gc = (lane & 3) * 2;
   const uint32_t smem = smem_u32(smem_raw);
   const int group = a.group, tok = MT / group;
-  const long long U = prefix_total(a, tok);
+  const long long U = prefix_total<PREFIX_N>(a, tok);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = U;
   const int ctas = prefix_ctas(U, gridDim.x);
   if (blockIdx.x >= ctas) return;
   const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
   const size_t width = (size_t)a.kv_heads * HD;
   const float sl = a.scale * 1.4426950408889634f;  // scores in log2 units
-  PrefixPos pos;
+  PrefixPos<PREFIX_N> pos;
   pos.find(a, tok, lo);
   for (long long u = lo; u < hi;) {
     if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
       set_err(a.status, DEV_BAD_INDEX);
       return;
     }
-    if (u == pos.u0) pos.publish(a, tok);
+    if (u == pos.u0) pos.publish(a, threadIdx.x, C::THREADS);
     const int b0 = (int)(u - pos.u0), b1 = (int)min((long long)pos.nb, b0 + (hi - u));
     const int rows = pos.nrow * group;
     const int np = pos.g.np, nk = np + pos.tail.y - pos.tail.x;
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
       for (int h = 0; h < 2; ++h) {
         const int r = wm * 16 + gr + h * 8;
         if (r >= rows) continue;
-        if ((lane & 3) == 0) a.ml[part * MT + r] = make_float2(m[h], l[h]);
+        if ((lane & 3) == 0) a.part_ml[part * MT + r] = make_float2(m[h], l[h]);
         float* dst = a.part + (part * MT + r) * HD + gc;
 #pragma unroll
         for (int i = 0; i < HD / 8; ++i)
@@ -306,7 +304,7 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
           acc.z = fmaf(w, v.z, acc.z);
           acc.w = fmaf(w, v.w, acc.w);
         }
-        if (c == 0) a.ml[part * MT + r] = make_float2(M, L);
+        if (c == 0) a.part_ml[part * MT + r] = make_float2(M, L);
         *reinterpret_cast<float4*>(a.part + (part * MT + r) * HD + c) = acc;
       }
     }

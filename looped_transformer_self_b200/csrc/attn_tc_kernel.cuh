@@ -1,11 +1,14 @@
-// lt_attn_prompt for bf16 on the 5th-generation tensor cores.
+// Attention of 128-row tiles on the 5th-generation tensor cores (bf16): the
+// kernel of lt_attn_prompt and lt_attn_prefix.
 //
-// One resident CTA per SM takes work items one after the other: two tiles of
-// 128 packed query rows of one key/value head, against the keys they see (or a
-// range of them, see `splits`), streamed in blocks of 128 through a ring of
-// shared-memory slots (TMA).  Warps 0-3 and 4-7 hold one tile each, a row per
-// thread; warp 8 loads, warps 9 and 10 issue the tiles' MMAs, warp 11 fetches
-// items.  Per tile and block:
+// A resident CTA per SM takes work items one after the other: two tiles of 128
+// packed query rows of one key/value head and a range of the keys they see, in
+// blocks of 128 that pass through a ring of shared-memory slots.  Warps 0-3 and
+// 4-7 hold one tile each, a row per thread; warps 9 and 10 issue the tiles'
+// MMAs, warp 11 fetches items, warp 8 loads queries and (prompt) keys and values
+// by TMA; for the slot cache warps 12-15 gather the rows (cp.async: one TMA
+// request per row ran at half the speed in the decode attention).  Per tile and
+// block:
 //   S = Q K^T      tcgen05.mma, both from shared memory, S in TMEM (fp32)
 //   P = 2^(S' - m) in registers, bf16 into the TMEM columns S stood in
 //   O += P V       tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
@@ -16,78 +19,30 @@
 // reference was taken: weights stay below 2^8 and sums are fp32, so nothing
 // overflows and the relative rounding of a weight is the same at any scale.
 //
-// Items come from the launch grid itself: a CTA that is done cancels a CTA that
-// has not started and takes its place (clusterlaunchcontrol), which balances
-// items of different lengths and lets loads and the first product of the next
-// item run under the softmax and output of the last.
+// What bounds it: a tile's chain of load S, maximum, 128 exponentials a thread,
+// product and next S, about 3500 cycles per block of both tiles at head size 128
+// against 2048 of the tensor pipe; the exponentials are 1500 of them.  Two
+// threads per row (16 softmax warps), exponentials on the FMA pipe (polynomial
+// of degree 5) and P in halves were measured and were not faster.
 #pragma once
 
 #include "attn_tc.cuh"
+#include "attn_prefix.cuh"
 #include "prompt_tile.cuh"
 
 namespace lt {
 
 template <int HD>
-struct PromptTc {
+struct TcShape {
   static constexpr int CHUNKS = (HD + 63) / 64;       // 128-byte column chunks of a row
   static constexpr int TILE = CHUNKS * 128 * 128;     // bytes of a 128-row tile
   static constexpr int SLOTS = HD > 64 ? 5 : 8;       // ring slots (K and V blocks in turn)
   static constexpr int OCOLS = CHUNKS * 64;           // TMEM columns of an output tile
-  static constexpr int THREADS = 384;                 // two softmax warpgroups, one for the rest
   static constexpr size_t TILES = (size_t)(2 + SLOTS) * TILE;  // queries, ring
 };
 
-constexpr int PROMPT_ITEMS = 3;  // items handed over ahead
-
-struct PromptItem {
-  int q0, k0, lq, lk;       // the sequence
-  int tile, kh, split, idx; // its pair of tiles, head, key range, place of its partial
-};
-struct PromptSmem {
-  PromptItem item[PROMPT_ITEMS];
-  alignas(16) uint4 clc;  // answer of a cancel request
-  uint64_t clc_full, loaded;
-  uint64_t item_full[PROMPT_ITEMS], item_empty[PROMPT_ITEMS];
-  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2][4], o_done[2], turn[2], fin;
-  uint32_t tmem;
-  int abort_flag;
-  int poison[4];  // by item: (its number + 1) once a masked block held an infinity or NaN among its values
-};
-
-template <int HD>
-constexpr size_t prompt_smem() { return PromptTc<HD>::TILES + sizeof(PromptSmem); }
-
-// What an item covers: per tile first token, tokens and blocks, and the ring's
-// blocks jb .. jb + n - 1.  The tiles share every block (step 1), except that an
-// item of a cut pair whose second tile is empty gives its rows to both, which
-// take the blocks in turn (step 2) and leave a partial each.
-struct PromptSpan {
-  int t0[2], nt[2], nb[2], n, jb, step;
-  __device__ __forceinline__ PromptSpan(const PromptItem& it, int tok, int splits) {
-    int full[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      t0[i] = (it.tile * 2 + i) * tok;
-      nt[i] = max(0, min(tok, it.lq - t0[i]));
-      full[i] = nt[i] ? cdiv(max(0, it.lk - it.lq + t0[i] + nt[i]), 128) : 0;
-    }
-    const int chunk = cdiv(max(full[0], full[1]), splits);
-    jb = it.split * chunk;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) nb[i] = max(0, min(full[i] - jb, chunk));
-    n = max(nb[0], nb[1]);
-    step = 1;
-    if (splits > 1 && nt[1] == 0) {
-      step = 2;
-      t0[1] = t0[0];
-      nt[1] = nt[0];
-      nb[1] = n >> 1;
-      nb[0] = n - nb[1];
-    }
-  }
-  // ring block of the tile's k-th block, from jb
-  __device__ __forceinline__ int at(int t, int k) const { return step == 2 ? 2 * k + t : k; }
-};
+constexpr int TC_ITEMS = 3;      // items handed over ahead
+constexpr int TC_VALID = 8;      // blocks whose marks of present keys are kept
 
 // Two fp32 operations per instruction.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -165,13 +120,129 @@ __device__ __forceinline__ int clc_answer(uint32_t at) {
   return ok ? (int)x : -1;
 }
 
-template <int HD>
-__global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
-    k_attn_prompt_tc(PromptArgs a, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv) {
-  using C = PromptTc<HD>;
+// What an item covers: per tile first token, tokens and blocks, and the ring's
+// blocks jb .. jb + n - 1.  The tiles share every block (step 1), except that
+// where the second tile is empty its rows may be the first's (step 2): then the
+// tiles take the blocks in turn and leave a partial each.
+struct TcSpan {
+  int t0[2], nt[2], nb[2], n, jb, step;
+  __device__ __forceinline__ void share_rows() {
+    step = 2;
+    t0[1] = t0[0];
+    nt[1] = nt[0];
+    nb[1] = n >> 1;
+    nb[0] = n - nb[1];
+  }
+  // ring block of the tile's k-th block, from jb
+  __device__ __forceinline__ int at(int t, int k) const { return step == 2 ? 2 * k + t : k; }
+};
+
+// lt_attn_prompt: a pair of tiles of one sequence, or one of `splits` ranges of
+// the keys it sees.  Items are the launch's CTAs: one that is done cancels one
+// that has not started and takes its place (clusterlaunchcontrol), which
+// balances items of different lengths and lets loads and the first product of
+// the next item run under the softmax and output of the last.
+struct PromptItem {
+  int q0, k0, lq, lk;        // the sequence
+  int tile, kh, split, part; // its pair of tiles, head, key range, place of its partial
+};
+struct PromptWork {
+  using Args = PromptArgs;
+  using Item = PromptItem;
+  static constexpr bool GATHER = false;
+  static constexpr int THREADS = 384;
+  static __device__ __forceinline__ bool partial(const Args& a) { return a.splits > 1; }
+  static __device__ __forceinline__ TcSpan span(const Item& it, int tok, int splits) {
+    TcSpan s;
+    int full[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.t0[i] = (it.tile * 2 + i) * tok;
+      s.nt[i] = max(0, min(tok, it.lq - s.t0[i]));
+      full[i] = s.nt[i] ? cdiv(max(0, it.lk - it.lq + s.t0[i] + s.nt[i]), 128) : 0;
+    }
+    const int chunk = cdiv(max(full[0], full[1]), splits);
+    s.jb = it.split * chunk;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s.nb[i] = max(0, min(full[i] - s.jb, chunk));
+    s.n = max(s.nb[0], s.nb[1]);
+    s.step = 1;
+    if (splits > 1 && s.nt[1] == 0) s.share_rows();
+    return s;
+  }
+  static __device__ __forceinline__ TcSpan span(const Item& it, int tok, const Args& a) {
+    return span(it, tok, a.splits);
+  }
+};
+
+// lt_attn_prefix: a CTA's share of a tile's blocks (see attn_prefix.cuh).
+struct PrefixItem {
+  int q0, lq;             // first row, rows
+  int p0, np, tail0, nk;  // prefix list, its length, the rows' tail list, keys together
+  int jb, n;              // blocks
+  int tile, kh, part;     // tile >= 0; head, place of its partial
+};
+struct PrefixWork {
+  using Args = PrefixArgs;
+  using Item = PrefixItem;
+  static constexpr bool GATHER = true;
+  static constexpr int THREADS = 512;
+  static __device__ __forceinline__ bool partial(const Args&) { return true; }
+  static __device__ __forceinline__ TcSpan span(const Item& it, int tok, const Args&) {
+    TcSpan s;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.t0[i] = i * tok;
+      s.nt[i] = max(0, min(tok, it.lq - s.t0[i]));
+      s.nb[i] = s.nt[i] ? it.n : 0;
+    }
+    s.n = it.n;
+    s.jb = it.jb;
+    s.step = 1;
+    if (s.nt[1] == 0) s.share_rows();
+    return s;
+  }
+};
+
+template <class W>
+struct TcSmem {
+  typename W::Item item[TC_ITEMS];
+  alignas(16) uint4 clc;  // answer of a cancel request
+  uint64_t clc_full, loaded;
+  uint64_t item_full[TC_ITEMS], item_empty[TC_ITEMS];
+  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2][4], o_done[2], turn[2], fin;
+  uint32_t tmem;
+  int abort_flag;
+  int poison[4];  // by item: (its number + 1) once a masked block held an infinity or NaN among its values
+  uint64_t valid_full[W::GATHER ? TC_VALID : 1];
+  uint32_t valid[W::GATHER ? TC_VALID : 1][4];  // keys of a block that are there, one bit each
+};
+template <int HD, class W>
+constexpr size_t tc_smem() { return TcShape<HD>::TILES + sizeof(TcSmem<W>); }
+
+// Bits [lo, hi) of 32.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  lo = min(max(lo, 0), 32);
+  hi = min(max(hi, 0), 32);
+  const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1;
+  return lo == 32 ? 0u : below_hi & (0xffffffffu << lo);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+
+template <int HD, class W>
+__global__ void __launch_bounds__(W::THREADS, 1)
+    k_attn_tc(const __grid_constant__ typename W::Args a, const __grid_constant__ CUtensorMap mq,
+              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using C = TcShape<HD>;
+  using Item = typename W::Item;
+  constexpr bool GATHER = W::GATHER;
   extern __shared__ __align__(1024) char smem_raw[];
-  PromptSmem& sb = *reinterpret_cast<PromptSmem*>(smem_raw + C::TILES);
+  TcSmem<W>& sb = *reinterpret_cast<TcSmem<W>*>(smem_raw + C::TILES);
   if (smem_u32(smem_raw) & 1023) {  // swizzle atoms are 1024 bytes
     set_err(a.status, DEV_STATE);
     return;
@@ -194,12 +265,12 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
     mbar_init(fin, 2);
     mbar_init(smem_u32(&sb.clc_full), 1);
     mbar_init(smem_u32(&sb.loaded), 1);
-    for (int s = 0; s < PROMPT_ITEMS; ++s) {
+    for (int s = 0; s < TC_ITEMS; ++s) {
       mbar_init(smem_u32(&sb.item_full[s]), 1);
-      mbar_init(smem_u32(&sb.item_empty[s]), 11);  // eight softmax warps, the loader, two MMA warps
+      mbar_init(smem_u32(&sb.item_empty[s]), GATHER ? 15 : 11);  // eight softmax warps, the loaders, two MMA warps
     }
     for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(kv_full(s), 1);
+      mbar_init(kv_full(s), GATHER ? 128 : 1);
       mbar_init(kv_empty(s), 2);  // both tiles
     }
     for (int t = 0; t < 2; ++t) {
@@ -208,6 +279,8 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
       mbar_init(o_done(t), 1);
       mbar_init(smem_u32(&sb.turn[t]), 4);  // four warps of the other tile
     }
+    if (GATHER)
+      for (int i = 0; i < TC_VALID; ++i) mbar_init(smem_u32(&sb.valid_full[i]), 4);
     sb.abort_flag = 0;
     for (int i = 0; i < 4; ++i) sb.poison[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -228,49 +301,128 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
   auto slot_of = [&](int u) { return u % C::SLOTS; };
   auto par_of = [&](int u) { return (uint32_t)(u / C::SLOTS) & 1; };
   // the next item of this CTA (its `it`-th); false at the end
-  auto take = [&](int it, PromptItem& item) -> bool {
-    const int e = it % PROMPT_ITEMS;
-    if (!mbar_wait(smem_u32(&sb.item_full[e]), (uint32_t)(it / PROMPT_ITEMS) & 1, abort_flag)) return false;
+  auto take = [&](int it, Item& item) -> bool {
+    const int e = it % TC_ITEMS;
+    if (!mbar_wait(smem_u32(&sb.item_full[e]), (uint32_t)(it / TC_ITEMS) & 1, abort_flag)) return false;
     item = sb.item[e];
     return item.tile >= 0;
   };
-  auto give_back = [&](int it) { mbar_arrive(smem_u32(&sb.item_empty[it % PROMPT_ITEMS])); };
+  auto give_back = [&](int it) { mbar_arrive(smem_u32(&sb.item_empty[it % TC_ITEMS])); };
 
-  // 168 registers a thread at launch (3 warps per scheduler): the softmax warpgroups take 216, the
-  // last keeps 72 (216 + 216 + 72 = 3 * 168).
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  // Registers a thread: 168 at launch with three warps per scheduler, of which the softmax
+  // warpgroups take 216 and the third keeps 72 (216 + 216 + 72 = 3 * 168); 128 with four, 200, 200,
+  // 56 and 56 (= 4 * 128).
+  if (GATHER && warp >= 12) {
+    if constexpr (GATHER) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      // Keys 32 w + lane of every block: a lane holds one key's slot, and the warp copies the rows of
+      // its 32 keys, LPR lanes per row with a 16-byte piece each.  The slots of a lane's rows are
+      // spread once for keys and values.  A ring slot counts as full when the copies of all lanes have
+      // landed (the barrier follows them); the MMA warps put the proxy fence between the copies and
+      // their products.  Waiting for copies here delayed their use by up to three slots.
+      constexpr int PIECES = HD / 8, LPR = PIECES > 8 ? 16 : PIECES > 4 ? 8 : 4;
+      const int p = lane % LPR, r0 = lane / LPR * LPR;  // piece, first of the lane's LPR rows
+      const int w = warp - 12;
+      const size_t width = (size_t)a.kv_heads * HD, stride = 2 * width;
+      int u = 0;  // ring uses issued
+      bool ok = true;
+      Item item;
+      for (int it = 0;; ++it) {
+        ok = __all_sync(0xffffffffu, take(it, item));
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) give_back(it);
+        const __nv_bfloat16* base = (const __nv_bfloat16*)a.cache + (size_t)item.kh * HD;
+        auto fetch = [&](int j) {
+          const int x = (item.jb + j) * 128 + w * 32 + lane;
+          int s = -1;
+          if (j < item.n) {
+            if (x < item.np) s = __ldg(a.prefix + item.p0 + x);
+            else if (x < item.nk) s = __ldg(a.tail + item.tail0 + x - item.np);
+          }
+          return s >= 0 && s < a.n_slots ? s : -1;
+        };
+        int ahead = fetch(0);
+        for (int j = 0; ok && j < item.n; ++j) {
+          const int mine = ahead;
+          ahead = fetch(j + 1);
+          const uint32_t here = __ballot_sync(0xffffffffu, mine >= 0);
+          int slots[LPR];
+#pragma unroll
+          for (int i = 0; i < LPR; ++i) slots[i] = __shfl_sync(0xffffffffu, mine, r0 + i);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++u) {
+            const int s = slot_of(u);
+            if (u >= C::SLOTS &&
+                !(ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(s), par_of(u) ^ 1, abort_flag))))
+              break;
+            if (kv == 0 && lane == 0) {
+              const int b = (u >> 1) & (TC_VALID - 1);
+              sb.valid[b][w] = here;
+              mbar_arrive(smem_u32(&sb.valid_full[b]));
+            }
+            const uint32_t dst = ring + s * C::TILE + (w * 32 + r0) * 128 + (p >> 3) * 16384;
+            const __nv_bfloat16* src = base + (kv ? width : 0) + p * 8;
+            if (PIECES == LPR || p < PIECES) {
+              if (here == 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < LPR; ++i)
+                  cp_async16(dst + i * 128 + (((p & 7) ^ ((r0 + i) & 7)) << 4), src + (size_t)slots[i] * stride);
+              } else {  // absent keys' rows are zero
+#pragma unroll
+                for (int i = 0; i < LPR; ++i)
+                  cp_async16(dst + i * 128 + (((p & 7) ^ ((r0 + i) & 7)) << 4),
+                             src + (size_t)max(slots[i], 0) * stride, slots[i] >= 0);
+              }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(kv_full(s)) : "memory");
+          }
+        }
+        if (!ok) break;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // copies in flight land before the CTA leaves
+    }
+  } else if (warp >= 8) {
+    if constexpr (GATHER)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
       if (lane == 0) {
         int u = 0, qn = 0;
         bool ok = true;
-        PromptItem item;
+        Item item;
         for (int it = 0; ok && take(it, item); ++it) {
-          const PromptSpan sp(item, tok, a.splits);
-          const int ub = u;
-          for (; u < ub + 2 * sp.n; ++u) {
-            if (u == ub + 1) {  // the queries, behind the first key block
-              if (qn > 0 && !(ok = mbar_wait(q_empty, (uint32_t)(qn - 1) & 1, abort_flag))) break;
-              const int qt = (sp.nt[0] > 0) + (sp.nt[1] > 0);
-              mbar_expect_tx(q_full, (uint32_t)(qt * C::CHUNKS * tok * group * 128));
-              for (int t = 0; t < qt; ++t) {
-                const int at = item.q0 + sp.t0[t];
-                tma_load_4d(q_s + t * C::TILE, &mq, 0, item.kh * group, at, 0, q_full);
-                if (HD == 96) tma_load_4d(q_s + t * C::TILE + 16384, &mq, 64, item.kh * group, at, 0, q_full);
-              }
-              ++qn;
+          const TcSpan sp = W::span(item, tok, a);
+          auto load_q = [&] {
+            if (qn > 0 && !(ok = mbar_wait(q_empty, (uint32_t)(qn - 1) & 1, abort_flag))) return;
+            const int qt = (sp.nt[0] > 0) + (sp.nt[1] > 0);
+            mbar_expect_tx(q_full, (uint32_t)(qt * C::CHUNKS * tok * group * 128));
+            for (int t = 0; t < qt; ++t) {
+              const int at = item.q0 + sp.t0[t];
+              tma_load_4d(q_s + t * C::TILE, &mq, 0, item.kh * group, at, 0, q_full);
+              if (HD == 96) tma_load_4d(q_s + t * C::TILE + 16384, &mq, 64, item.kh * group, at, 0, q_full);
             }
-            const int s = slot_of(u);
-            if (u >= C::SLOTS && !(ok = mbar_wait(kv_empty(s), par_of(u) ^ 1, abort_flag))) break;
-            const CUtensorMap* m = ((u - ub) & 1) ? &mv : &mk;
-            const int key = item.k0 + (sp.jb + ((u - ub) >> 1)) * 128;
-            mbar_expect_tx(kv_full(s), C::TILE);
-            tma_load_4d(ring + s * C::TILE, m, 0, item.kh, key, 0, kv_full(s));
-            if (HD == 96) tma_load_4d(ring + s * C::TILE + 16384, m, 64, item.kh, key, 0, kv_full(s));
+            ++qn;
+          };
+          if constexpr (GATHER) {
+            load_q();
+          } else {
+            const int ub = u;
+            for (; ok && u < ub + 2 * sp.n; ++u) {
+              if (u == ub + 1) load_q();  // behind the first key block
+              const int s = slot_of(u);
+              if (!ok || (u >= C::SLOTS && !(ok = mbar_wait(kv_empty(s), par_of(u) ^ 1, abort_flag)))) break;
+              const CUtensorMap* m = ((u - ub) & 1) ? &mv : &mk;
+              const int key = item.k0 + (sp.jb + ((u - ub) >> 1)) * 128;
+              mbar_expect_tx(kv_full(s), C::TILE);
+              tma_load_4d(ring + s * C::TILE, m, 0, item.kh, key, 0, kv_full(s));
+              if (HD == 96) tma_load_4d(ring + s * C::TILE + 16384, m, 64, item.kh, key, 0, kv_full(s));
+            }
           }
           if (!ok) break;
           give_back(it);
-          mbar_arrive(smem_u32(&sb.loaded));
+          if constexpr (!GATHER) mbar_arrive(smem_u32(&sb.loaded));
         }
         if (*abort_flag) {  // copies in flight land before the CTA leaves
           int none = 0;
@@ -301,11 +453,11 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         }
       };
       bool ok = true;
-      PromptItem item;
+      Item item;
       for (int it = 0; ok; ++it) {
         ok = __all_sync(0xffffffffu, take(it, item));
         if (!ok) break;
-        const PromptSpan sp(item, tok, a.splits);
+        const TcSpan sp = W::span(item, tok, a);
         __syncwarp();
         if (lane == 0) give_back(it);
         if (sp.n == 0) continue;
@@ -320,6 +472,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           const int k_slot = slot;
           const uint32_t k_par = ring_par;
           if (j > 0 && !(ok = wait(kv_full(v_slot), v_par))) break;
+          if (GATHER) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           if (p_next > 0) {
             const uint64_t v = dv + (uint32_t)(v_slot * (C::TILE >> 4));
             const uint32_t par = (uint32_t)(done + p_next - 1) & 1;
@@ -340,6 +493,7 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           }
           if (j < sp.n) {
             if (!(ok = wait(kv_full(k_slot), k_par))) break;
+            if (GATHER) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             if (s_next < nb && j == sp.at(t, s_next)) {
               p_next = ++s_next;
               tc_fence_after();
@@ -378,45 +532,78 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
         __syncwarp();
       }
     } else {
-      // An item is asked for when the loads of the one before are out: the ring holds two blocks or
-      // more then, which covers the answer, and no CTA takes work that another could start sooner.
-      int idx = blockIdx.x, it = 0;
-      bool ok = true;
-      const uint32_t clc = smem_u32(&sb.clc), clc_full = smem_u32(&sb.clc_full);
       auto wait = [&](uint32_t bar, uint32_t par) {
         return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag)) != 0;
       };
-      for (uint32_t asked = 0;; ++asked) {
-        PromptTile pt;
-        const int pair = idx / a.splits;
-        const bool have = idx >= 0 && prompt_tile(a, pair / a.kv_heads, 2 * tok, pt);
-        if (have || idx < 0) {
-          const int e = it % PROMPT_ITEMS;
-          if (it >= PROMPT_ITEMS)
-            ok = wait(smem_u32(&sb.item_empty[e]), (uint32_t)(it / PROMPT_ITEMS - 1) & 1);
-          if (!ok) break;
-          if (lane == 0) {
+      auto hand_over = [&](int it, const Item& item) {
+        const int e = it % TC_ITEMS;
+        if (it >= TC_ITEMS && !wait(smem_u32(&sb.item_empty[e]), (uint32_t)(it / TC_ITEMS - 1) & 1)) return false;
+        if (lane == 0) {
+          sb.item[e] = item;
+          mbar_arrive(smem_u32(&sb.item_full[e]));
+        }
+        return true;
+      };
+      if constexpr (GATHER) {
+        const int rows = 2 * tok;  // of a pair of tiles
+        const long long U = prefix_total<128>(a, rows);
+        if (blockIdx.x == 0 && lane == 0) a.head[0] = U;
+        const int ctas = prefix_ctas(U, gridDim.x);
+        int it = 0;
+        if (blockIdx.x < ctas) {
+          const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
+          PrefixPos<128> pos;
+          pos.find(a, rows, lo);
+          for (long long u = lo; u < hi;) {
+            if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
+              set_err(a.status, DEV_BAD_INDEX);
+              break;
+            }
+            if (u == pos.u0) pos.publish(a, lane, 32, tok, pos.nrow <= tok);
+            const int b0 = (int)(u - pos.u0), n = (int)min((long long)pos.nb - b0, hi - u);
+            if (!hand_over(it, PrefixItem{pos.row0, pos.nrow, pos.g.p0, pos.g.np, pos.tail.x,
+                                          pos.g.np + pos.tail.y - pos.tail.x, b0, n, 0, pos.kh,
+                                          (int)blockIdx.x + pos.t}))
+              break;
+            ++it;
+            u += n;
+            if (u < hi) pos.next(a, rows);
+          }
+        }
+        hand_over(it, PrefixItem{0, 0, 0, 0, 0, 0, 0, 0, -1, 0, 0});
+      } else {
+        // An item is asked for when the loads of the one before are out: the ring holds two blocks or
+        // more then, which covers the answer, and no CTA takes work that another could start sooner.
+        int idx = blockIdx.x, it = 0;
+        const uint32_t clc = smem_u32(&sb.clc), clc_full = smem_u32(&sb.clc_full);
+        for (uint32_t asked = 0;; ++asked) {
+          PromptTile pt;
+          const int pair = idx / a.splits;
+          const bool have = idx >= 0 && prompt_tile(a, pair / a.kv_heads, 2 * tok, pt);
+          if (have || idx < 0) {
             PromptItem item = {0, 0, 0, 0, -1, 0, 0, 0};
             if (have) item = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, pair % a.kv_heads, idx % a.splits, idx};
-            sb.item[e] = item;
-            mbar_arrive(smem_u32(&sb.item_full[e]));
+            if (!hand_over(it, item)) break;
+            if (idx < 0 || !wait(smem_u32(&sb.loaded), (uint32_t)it & 1)) break;
+            ++it;
           }
-          if (idx < 0 || !wait(smem_u32(&sb.loaded), (uint32_t)it & 1)) break;
-          ++it;
+          if (lane == 0) clc_request(clc, clc_full);
+          __syncwarp();
+          if (!wait(clc_full, asked & 1)) {  // nothing writes to shared memory after the CTA is gone
+            int none = 0;
+            mbar_wait(clc_full, asked & 1, &none);
+            break;
+          }
+          idx = clc_answer(clc);
+          __syncwarp();
         }
-        if (lane == 0) clc_request(clc, clc_full);
-        __syncwarp();
-        if (!wait(clc_full, asked & 1)) {  // nothing writes to shared memory after the CTA is gone
-          int none = 0;
-          mbar_wait(clc_full, asked & 1, &none);
-          break;
-        }
-        idx = clc_answer(clc);
-        __syncwarp();
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (GATHER)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
@@ -440,16 +627,28 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
       if (lane == 0) mbar_arrive(other_turn);
     };
     for (int it = 0; ok; ++it) {
-      PromptItem item;
+      Item item;
       ok = __all_sync(0xffffffffu, take(it, item));
       if (!ok) break;
       if (lane == 0) give_back(it);
-      const PromptSpan sp(item, tok, a.splits);
+      const TcSpan sp = W::span(item, tok, a);
       const int t0 = t ? sp.t0[1] : sp.t0[0], nt = t ? sp.nt[1] : sp.nt[0], nb = t ? sp.nb[1] : sp.nb[0];
-      const int ctx = item.lk - item.lq;
       const bool valid = tl < nt && r < tok * group;
-      const int see = valid ? ctx + t0 + tl + 1 : 0;  // keys this row sees (may be <= 0)
-      const int see_first = ctx + t0 + 1;             // keys the tile's first row sees
+      // Keys a row sees: [0, see) and, of the slot cache, also [own.x, own.y).  Keys from `shared` on
+      // are not seen by all rows of the tile.
+      int see, shared;
+      int2 own = {0, 0};
+      if constexpr (GATHER) {
+        see = shared = item.np;
+        if (valid) {
+          const int2 t2 = off_range(a.tail_off, item.q0 + t0 + tl, a.n_tail, a.status);
+          own = {item.np + t2.x - item.tail0, item.np + t2.y - item.tail0};
+        }
+      } else {
+        const int ctx = item.lk - item.lq;
+        see = valid ? ctx + t0 + tl + 1 : 0;  // may be <= 0
+        shared = ctx + t0 + 1;
+      }
       float m = -INFINITY, l = 0.f;                   // m: reference maximum of the raw scores
       for (int jj = 0; jj < nb; ++jj) {
         const int jr = sp.at(t, jj), j = sp.jb + jr, ph = done + jj;
@@ -459,27 +658,41 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, x + c * 32);
         tmem_wait_ld();
-        const bool masked = (j + 1) * 128 > see_first;
+        const bool mixed = (j + 1) * 128 > shared;  // holds keys that some row does not see
+        bool masked = mixed;
+        const uint32_t* there = nullptr;
+        if constexpr (GATHER) {
+          // the loads are fewer than TC_VALID blocks ahead, so the marks stay
+          const int b = (ub >> 1) + jr;
+          if (!(ok = wait(smem_u32(&sb.valid_full[b & (TC_VALID - 1)]), (uint32_t)(b / TC_VALID) & 1))) break;
+          there = sb.valid[b & (TC_VALID - 1)];
+          masked = mixed || (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
+        }
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int lim = min(max(see - j * 128 - c * 32, 0), 32);
-            const uint32_t hide = lim == 32 ? 0u : 0xffffffffu << lim;
+            const int x0 = j * 128 + c * 32;
+            uint32_t seen = bit_range(0, see - x0);
+            if constexpr (GATHER) seen = (seen | bit_range(own.x - x0, own.y - x0)) & there[c];
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (hide & (1u << i)) x[c * 32 + i] = 0xff800000u;  // -inf
+              if (!(seen & (1u << i))) x[c * 32 + i] = 0xff800000u;  // -inf
           }
+        }
+        if (mixed) {
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
           // that see them at the end.  A thread goes over one key's row.
           const int u = ub + 2 * jr + 1;
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
           char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
-          const bool gone = j * 128 + r >= item.lk;
+          bool gone = false;  // an absent slot's row is zero already
+          if constexpr (!GATHER) gone = j * 128 + r >= item.lk;
           uint32_t bad = 0;
 #pragma unroll
-          for (int k = 0; k < C::CHUNKS * 8; ++k) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * 16384 + ((k + r) & 7) * 16);
+          for (int k = 0; k < HD / 8; ++k) {
+            // a key's 16-byte pieces lie at places given by its row (the swizzle)
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4));
             bad |= nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) | nonfinite_bits(v.w);
           }
           if (gone || bad) {
@@ -488,8 +701,8 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
               __threadfence_block();  // a warp that finds the value gone finds the flag set
             }
 #pragma unroll 1
-            for (int k = 0; k < C::CHUNKS * 8; ++k) {
-              uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + (k & 7) * 16);
+            for (int k = 0; k < HD / 8; ++k) {
+              uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4));
               uint4 v = *q;
               if (gone) v = make_uint4(0u, 0u, 0u, 0u);
               drop_nonfinite(v.x);
@@ -562,20 +775,29 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
       }
       turns += most;
       if (!ok) break;
-      if (nt > 0 && (nb > 0 || a.splits == 1)) {
+      const bool partial = W::partial(a);
+      if (nt > 0 && (nb > 0 || !partial)) {
         if (nb > 0) {
           if (!(ok = wait(o_done(t), (done + nb - 1) & 1))) break;
           tc_fence_after();
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t prow = (size_t)item.idx * 256 + t * 128 + r;  // row of the partial (splits > 1)
-        if (a.splits > 1 && valid) a.part_ml[prow] = make_float2(m * sl, l);
+        const size_t prow = (size_t)item.part * 256 + t * 128 + r;  // row of the partial
+        if (partial && valid) a.part_ml[prow] = make_float2(m * sl, l);
         __nv_bfloat16* o = (__nv_bfloat16*)a.o + (size_t)(item.q0 + t0 + tl) * a.so +
                            (size_t)(item.kh * group + r % group) * HD;
         const bool poison = nb > 0 && *(volatile int*)&sb.poison[it & 3] == it + 1;
-        // masked keys of either tile start here
-        const int from = max(max(0, (ctx + sp.t0[0] + 1) & ~127), sp.jb * 128);
-        const int to = min(ctx + t0 + nt, (sp.jb + sp.n) * 128);
+        // keys of mixed blocks of either tile
+        int from, to;
+        if constexpr (GATHER) {
+          from = item.np & ~127;
+          to = item.nk;
+        } else {
+          from = max(0, (item.lk - item.lq + sp.t0[0] + 1) & ~127);
+          to = item.lk - item.lq + t0 + nt;
+        }
+        from = max(from, sp.jb * 128);
+        to = min(to, (sp.jb + sp.n) * 128);
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t x[32];
@@ -589,21 +811,28 @@ __global__ void __launch_bounds__(PromptTc<HD>::THREADS, 1)
           if (poison) {
             for (int key = from; key < to; ++key) {
               if (sp.step == 2 && (((key >> 7) - sp.jb) & 1) != t) continue;  // the other tile's
-              const __nv_bfloat16* v =
-                  (const __nv_bfloat16*)a.v + (size_t)(item.k0 + key) * a.sv + (size_t)item.kh * HD + c;
+              const __nv_bfloat16* v;
+              if constexpr (GATHER) {
+                const int slot = key < item.np ? __ldg(a.prefix + item.p0 + key) : __ldg(a.tail + item.tail0 + key - item.np);
+                if (slot < 0 || slot >= a.n_slots) continue;
+                v = (const __nv_bfloat16*)a.cache + ((size_t)slot * 2 + 1) * a.kv_heads * HD;
+              } else {
+                v = (const __nv_bfloat16*)a.v + (size_t)(item.k0 + key) * a.sv;
+              }
+              v += (size_t)item.kh * HD + c;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const float f = __bfloat162float(v[i]);
-                if (!(fabsf(f) < INFINITY) && key < see) x[i] = __float_as_uint(__uint_as_float(x[i]) + f);
+                if (!(fabsf(f) < INFINITY) && (key < see || (key >= own.x && key < own.y))) x[i] = __float_as_uint(__uint_as_float(x[i]) + f);
               }
             }
           }
           if (!valid) continue;
-          if (a.splits > 1) {
+          if (partial) {
             float* dst = a.part + prow * HD + c;
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_global32(dst + 8 * i, x + 8 * i);
-          } else {
+          } else if constexpr (!GATHER) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               x[i] = pack_bf16(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
@@ -649,7 +878,7 @@ __global__ void __launch_bounds__(256) k_attn_prompt_join(PromptArgs a, int part
   const int t = row >> 7, r = row & 127, token = (pt.tile * 2 + t) * tok + r / a.group;
   if ((int)threadIdx.x >= ROWS * PER || row >= 256 || r >= tok * a.group || token >= pt.lq) return;
   const PromptItem it = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, kh, 0, 0};
-  const PromptSpan whole(it, tok, 1);
+  const TcSpan whole = PromptWork::span(it, tok, 1);
   const int blocks = t ? whole.nb[1] : whole.nb[0], chunk = cdiv(whole.n, a.splits);
   // a range's partial, or its two where both tiles took the rows (blocks in turn)
   const int two = whole.nt[1] == 0 ? 2 : 1;
@@ -692,45 +921,6 @@ __global__ void __launch_bounds__(256) k_attn_prompt_join(PromptArgs a, int part
   *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + (size_t)(pt.q0 + token) * a.so +
                             (size_t)(kh * a.group + r % a.group) * HD + c) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-}
-
-template <int HD>
-static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
-  using C = PromptTc<HD>;
-  const int tok = 128 / a.group;
-  CUtensorMap mq, mk, mv;
-  // no keys: nothing is loaded, and the maps stand on the queries
-  const void* k = a.n_kv > 0 ? a.k : a.q;
-  const void* v = a.n_kv > 0 ? a.v : a.q;
-  const long long nk = a.n_kv > 0 ? a.n_kv : 1;
-  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_q, a.sq, a.group, tok) ||
-      attn_tmap(&mk, k, HD, a.kv_heads, nk, a.sk, 1, 128) || attn_tmap(&mv, v, HD, a.kv_heads, nk, a.sv, 1, 128))
-    return LT_ERR_CUDA;
-  static bool set[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !set[dev]) {
-    if (cudaFuncSetAttribute(k_attn_prompt_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prompt_smem<HD>()) !=
-        cudaSuccess)
-      return LT_ERR_CUDA;
-    if (dev >= 0 && dev < 64) set[dev] = true;
-  }
-  const unsigned pairs = (unsigned)prompt_pairs(a.n_q, a.n_seqs, a.group) * a.kv_heads;
-  k_attn_prompt_tc<HD><<<pairs * a.splits, C::THREADS, prompt_smem<HD>(), st>>>(a, mq, mk, mv);
-  if (a.splits > 1) {
-    cudaLaunchConfig_t cfg = {};
-    const int parts = cdiv(256, prompt_join_rows<HD>());
-    cfg.gridDim = dim3(pairs * parts);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_attn_prompt_join<HD>, a, parts) != cudaSuccess) return LT_ERR_CUDA;
-  }
-  return cudaGetLastError() == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 }  // namespace lt

@@ -3,6 +3,7 @@
 // of one committed prefix, or the samples of one prompt), and each row's own
 // tail is read for it alone.
 #include "../../include/looped_spec.h"
+#include <stdlib.h>
 #include "attn_prefix_mma.cuh"
 
 namespace lt {
@@ -14,21 +15,21 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
   SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
   __shared__ int slot[PREFIX_N];
   const int tok = SIMT_M / a.group, group = a.group;
-  const long long U = prefix_total(a, tok);
+  const long long U = prefix_total<PREFIX_N>(a, tok);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = U;
   const int ctas = prefix_ctas(U, gridDim.x);
   if (blockIdx.x >= ctas) return;
   const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
   const size_t width = (size_t)a.kv_heads * HD;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  PrefixPos pos;
+  PrefixPos<PREFIX_N> pos;
   pos.find(a, tok, lo);
   for (long long u = lo; u < hi;) {
     if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
       set_err(a.status, DEV_BAD_INDEX);
       return;
     }
-    if (u == pos.u0) pos.publish(a, tok);
+    if (u == pos.u0) pos.publish(a, threadIdx.x, SIMT_THREADS);
     const int b0 = (int)(u - pos.u0), b1 = (int)min((long long)pos.nb, b0 + (hi - u));
     const int rows = pos.nrow * group, h0 = pos.kh * group;
     const T* q = (const T*)a.q + (size_t)pos.row0 * a.sq + (size_t)h0 * HD;
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= rows) continue;
-      if (tx == 0) a.ml[part * SIMT_M + r] = make_float2(st.m[i] * 1.4426950408889634f, st.l[i]);
+      if (tx == 0) a.part_ml[part * SIMT_M + r] = make_float2(st.m[i] * 1.4426950408889634f, st.l[i]);
       float* o = a.part + (part * SIMT_M + r) * HD;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c)
@@ -90,8 +91,10 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
 // sum_i 2^(m_i - M) l_i.  One warp per (row, head).
 template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int grid) {
+  constexpr int PER = HD / 32;
   const int row = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (h >= a.heads) return;
+  pdl_wait();
   // rows before the first group or behind the last one are left as they were
   const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
   if (row < first || row >= last) return;
@@ -109,45 +112,84 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
     return;
   }
   const int ctas = prefix_ctas(U, grid);
-  const int c0 = prefix_cta_of(u0, U, ctas), c1 = prefix_cta_of(u0 + tt.z - 1, U, ctas);
-  float M = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, a.ml[(size_t)(c + t) * MT + r].x);
-  M = warp_max(M);
-  if (M == -INFINITY) M = 0.f;  // a row that sees nothing: its sum is 0
-  float l = 0.f, o[HD / 32];
+  const long long u1 = u0 + tt.z;
+  const int c0 = prefix_cta_of(u0, U, ctas), c1 = prefix_cta_of(u1 - 1, U, ctas), two = rt.w == 2 ? 2 : 1;
+  float M = -INFINITY, l = 0.f, o[PER];
 #pragma unroll
-  for (int i = 0; i < HD / 32; ++i) o[i] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const size_t p = (size_t)(c + t) * MT + r;
-    const float2 v = a.ml[p];
-    const float w = exp2f(v.x - M);
-    l += w * v.y;
-    const float* src = a.part + p * HD + lane * (HD / 32);
+  for (int i = 0; i < PER; ++i) o[i] = 0.f;
+  constexpr int B = 8;  // partials in flight
+  for (int k0 = 0; k0 < (c1 - c0 + 1) * two; k0 += B) {
+    float2 ml[B];
+    float v[B][PER];
 #pragma unroll
-    for (int i = 0; i < HD / 32; ++i) o[i] = fmaf(w, src[i], o[i]);
+    for (int k = 0; k < B; ++k) {
+      const int c = c0 + (k0 + k) / two, e = (k0 + k) % two;
+      // the second partial of a part of one block is not there
+      const bool there = c <= c1 && (e == 0 || min(u1, prefix_u0(c + 1, U, ctas)) - max(u0, prefix_u0(c, U, ctas)) > 1);
+      const size_t p = (size_t)(c + t) * MT + e * (MT / 2) + r;
+      ml[k] = there ? a.part_ml[p] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[k][i] = there ? a.part[p * HD + lane * PER + i] : 0.f;
+    }
+    float mx = M;
+#pragma unroll
+    for (int k = 0; k < B; ++k) mx = max_nan(mx, ml[k].x);
+    const float ms = mx == -INFINITY ? 0.f : mx, f = ex2(M - ms);  // nothing seen yet: the sum is 0
+    M = mx;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) o[i] *= f;
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const float w = ex2(ml[k].x - ms);
+      l += w * ml[k].y;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[k][i], o[i]);
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* dst = (T*)a.o + (size_t)row * a.so + (size_t)h * HD + lane * (HD / 32);
+  T* dst = (T*)a.o + (size_t)row * a.so + (size_t)h * HD + lane * PER;
 #pragma unroll
-  for (int i = 0; i < HD / 32; ++i) dst[i] = from_f<T>(o[i] * inv);
+  for (int i = 0; i < PER; ++i) dst[i] = from_f<T>(o[i] * inv);
+}
+
+template <typename T, int HD, int MT>
+static cudaError_t prefix_merge(const PrefixArgs& a, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_rows, cdiv(a.heads, 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attn_prefix_merge<T, HD, MT>, a, grid);
 }
 
 template <int HD>
 static cudaError_t prefix_f32(const PrefixArgs& a, int grid, cudaStream_t st) {
-  cudaFuncSetAttribute(k_attn_prefix_simt<float, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)sizeof(SimtSmem<HD>));
+  if (cudaError_t e = allow_smem((const void*)k_attn_prefix_simt<float, HD>, sizeof(SimtSmem<HD>))) return e;
   k_attn_prefix_simt<float, HD><<<grid, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
-  k_attn_prefix_merge<float, HD, SIMT_M><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
-  return cudaGetLastError();
+  return prefix_merge<float, HD, SIMT_M>(a, grid, st);
 }
 
 template <int HD, int MT>
 static cudaError_t prefix_mma(const PrefixArgs& a, int grid, cudaStream_t st) {
   using C = PrefixMma<HD, MT>;
-  cudaFuncSetAttribute(k_attn_prefix_mma<HD, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+  if (cudaError_t e = allow_smem((const void*)k_attn_prefix_mma<HD, MT>, C::SMEM)) return e;
   k_attn_prefix_mma<HD, MT><<<grid, C::THREADS, C::SMEM, st>>>(a);
-  k_attn_prefix_merge<__nv_bfloat16, HD, MT><<<dim3(a.n_rows, cdiv(a.heads, 8)), 256, 0, st>>>(a, grid);
-  return cudaGetLastError();
+  return prefix_merge<__nv_bfloat16, HD, MT>(a, grid, st);
+}
+
+template <int HD>
+static cudaError_t prefix_tc(const PrefixArgs& a, int grid, cudaStream_t st) {
+  using W = PrefixWork;
+  CUtensorMap mq;
+  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_rows, a.sq, a.group, 128 / a.group)) return cudaErrorInvalidValue;
+  if (cudaError_t e = allow_smem((const void*)k_attn_tc<HD, W>, tc_smem<HD, W>())) return e;
+  k_attn_tc<HD, W><<<grid, W::THREADS, tc_smem<HD, W>(), st>>>(a, mq, mq, mq);
+  return prefix_merge<__nv_bfloat16, HD, 256>(a, grid, st);
 }
 
 template <int HD>
@@ -156,7 +198,8 @@ static cudaError_t prefix_any(int dtype, int mt, const PrefixArgs& a, int grid, 
   switch (mt) {
     case 16: return prefix_mma<HD, 16>(a, grid, st);
     case 32: return prefix_mma<HD, 32>(a, grid, st);
-    default: return prefix_mma<HD, 64>(a, grid, st);
+    case 64: return prefix_mma<HD, 64>(a, grid, st);
+    default: return prefix_tc<HD>(a, grid, st);
   }
 }
 
@@ -174,9 +217,11 @@ static PrefixPlan prefix_plan(int dtype, int n_rows, int n_groups, int n_heads, 
     // the smallest tile that holds an average group's packed rows (a group may take several tiles)
     const long long avg = (long long)group * n_rows / (n_groups > 0 ? n_groups : 1);
     p.mt = avg <= 16 && group <= 16 ? 16 : avg <= 32 && group <= 32 ? 32 : 64;
+    if (getenv("KIND") && atoi(getenv("KIND"))) p.mt = 256;
   }
-  p.grid = 2 * attn_sm_count();
-  p.max_tiles = (long long)n_kv_heads * (n_rows / (p.mt / group) + (long long)n_groups);
+  const int tok = p.mt == 256 ? 2 * (128 / group) : p.mt / group;
+  p.grid = (p.mt == 256 ? 1 : 2) * attn_sm_count();
+  p.max_tiles = (long long)n_kv_heads * (n_rows / tok + (long long)n_groups);
   const size_t slots = (size_t)p.max_tiles + p.grid;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.tile_at = 256;

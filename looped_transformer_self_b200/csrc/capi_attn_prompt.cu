@@ -3,7 +3,7 @@
 // pieces).  Query t of a sequence with lq queries and lk keys sees keys
 // 0 .. lk - lq + t.
 #include "../../include/looped_spec.h"
-#include "attn_prompt_tc.cuh"
+#include "attn_tc_kernel.cuh"
 
 namespace lt {
 
@@ -53,10 +53,40 @@ template <typename T, int HD>
 static cudaError_t prompt_simt(const PromptArgs& a, cudaStream_t st) {
   const int tok = SIMT_M / a.group;
   const unsigned tiles = (unsigned)(a.n_q / tok + a.n_seqs);
-  cudaFuncSetAttribute(k_attn_prompt_simt<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       (int)sizeof(SimtSmem<HD>));
+  if (cudaError_t e = allow_smem((const void*)k_attn_prompt_simt<T, HD>, sizeof(SimtSmem<HD>))) return e;
   k_attn_prompt_simt<T, HD><<<tiles * a.kv_heads, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
   return cudaGetLastError();
+}
+
+template <int HD>
+static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
+  using W = PromptWork;
+  const int tok = 128 / a.group;
+  CUtensorMap mq, mk, mv;
+  // no keys: nothing is loaded, and the maps stand on the queries
+  const void* k = a.n_kv > 0 ? a.k : a.q;
+  const void* v = a.n_kv > 0 ? a.v : a.q;
+  const long long nk = a.n_kv > 0 ? a.n_kv : 1;
+  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_q, a.sq, a.group, tok) ||
+      attn_tmap(&mk, k, HD, a.kv_heads, nk, a.sk, 1, 128) || attn_tmap(&mv, v, HD, a.kv_heads, nk, a.sv, 1, 128))
+    return LT_ERR_CUDA;
+  if (allow_smem((const void*)k_attn_tc<HD, W>, tc_smem<HD, W>()) != cudaSuccess) return LT_ERR_CUDA;
+  const unsigned pairs = (unsigned)prompt_pairs(a.n_q, a.n_seqs, a.group) * a.kv_heads;
+  k_attn_tc<HD, W><<<pairs * a.splits, W::THREADS, tc_smem<HD, W>(), st>>>(a, mq, mk, mv);
+  if (a.splits > 1) {
+    cudaLaunchConfig_t cfg = {};
+    const int parts = cdiv(256, prompt_join_rows<HD>());
+    cfg.gridDim = dim3(pairs * parts);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, k_attn_prompt_join<HD>, a, parts) != cudaSuccess) return LT_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 template <int HD>
