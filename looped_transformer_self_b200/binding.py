@@ -254,60 +254,60 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _launch(device, stream, what, fn, *args) -> None:
-    """fn(*args, stream handle) with `device` current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index is None or device.index == torch.cuda.current_device():
-        check(fn(*args, stream.cuda_stream), what)
+def _launch(dev: int, stream, what, fn, *args) -> None:
+    """fn(*args, stream handle) with device `dev` current."""
+    handle = (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if dev == torch._C._cuda_getDevice():
+        code = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            check(fn(*args, stream.cuda_stream), what)
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code != 0:
+        raise LoopedSpecError(code, what)
 
 
-def _attn_dtype(t: torch.Tensor) -> int:
-    assert t.dtype in (torch.float32, torch.bfloat16), t.dtype
-    return LT_F32 if t.dtype == torch.float32 else LT_BF16
+# One attribute read of a tensor costs about a tenth of a microsecond and a call of a
+# few microseconds' work makes dozens, so the checks below read each once.
+
+def _rows(t: torch.Tensor, name: str, dtype, dev: int):
+    """Shape and row stride of [rows][heads][head_dim] (or [rows][columns]) of this
+    type and device whose rows are contiguous; a single row's own stride may be
+    anything."""
+    assert t.dtype is dtype and t.get_device() == dev, name
+    shape, st = t.shape, t.stride()
+    row = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    if st[-1] != 1 or (len(shape) == 3 and st[1] != shape[2]):  # sizes of 0 or 1 may have any stride
+        assert shape[0] == 0 or (st[-1] == 1 or shape[-1] <= 1) and (
+            len(shape) == 2 or st[1] == shape[2] or shape[1] <= 1), name
+    return shape, st[0] if shape[0] > 1 else row
 
 
-def _heads(t: torch.Tensor) -> None:
-    """[tokens][heads][head_dim] whose heads lie side by side in a token's row."""
-    assert t.dim() == 3 and (t.numel() == 0 or t.stride(2) == 1)
-    assert t.shape[1] <= 1 or t.numel() == 0 or t.stride(1) == t.shape[2]
+def _list(t: torch.Tensor, name: str, dtype, dev: int):
+    """Address and length of a contiguous list."""
+    assert t.dtype is dtype and t.get_device() == dev and t.dim() == 1 and t.is_contiguous(), name
+    return t.data_ptr(), t.numel()
 
 
-def _row(t: torch.Tensor) -> int:
-    """Stride between rows; a single row's own stride may be anything."""
-    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])
+_I32, _F32 = torch.int32, torch.float32
+_DTYPE = {torch.float32: LT_F32, torch.bfloat16: LT_BF16}
 
 
-def _off(t: torch.Tensor, device) -> int:
-    assert t.dtype == torch.int32 and t.dim() == 1 and t.is_contiguous() and t.device == device
-    assert t.numel() >= 1
-    return t.data_ptr()
+def _status_ptr(status, dev: int):
+    return None if status is None else _list(status, "status", _I32, dev)[0]
 
 
-def _list(t: torch.Tensor, dtype, device) -> int:
-    assert t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and t.device == device
-    return t.data_ptr()
-
-
-def _status_ptr(status, device):
-    if status is None:
-        return None
-    assert status.dtype == torch.int32 and status.numel() >= 1 and status.device == device
-    return status.data_ptr()
+def _scratch(need_fn, dtype, device, stream, *sizes) -> torch.Tensor:
+    need = _sz()
+    check(need_fn(dtype, *sizes, ctypes.byref(need)), "scratch bytes")
+    return _new(need.value, torch.uint8, device, stream)
 
 
 def attn_prompt_scratch(q: torch.Tensor, k: torch.Tensor, q_off: torch.Tensor,
                         stream=None) -> torch.Tensor:
-    """Scratch memory for attn_prompt calls of these sizes (or fewer tokens and
-    sequences), on one stream or in one captured graph at a time."""
-    need = _sz()
-    check(lib().lt_attn_prompt_scratch_bytes(_attn_dtype(q), q.shape[0], q_off.numel() - 1, q.shape[1],
-                                             k.shape[1], q.shape[2], ctypes.byref(need)),
-          "lt_attn_prompt_scratch_bytes")
-    return _new(need.value, torch.uint8, q.device, stream)
+    """Scratch memory for attn_prompt calls of these sizes, on one stream or in
+    one captured graph at a time."""
+    return _scratch(lib().lt_attn_prompt_scratch_bytes, _DTYPE[q.dtype], q.device, stream, q.shape[0],
+                    q_off.numel() - 1, q.shape[1], k.shape[1], q.shape[2])
 
 
 def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off: torch.Tensor,
@@ -318,37 +318,39 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off: torch.
     k and v [n_kv][H_kv][hd] (token strides free), offsets device int32.  Sequence
     s's last query sees all of its keys.  Rows of `out` outside the sequences
     keep their values (an `out` made here has none there).  scale: 1/sqrt(hd)."""
-    assert q.is_cuda and k.device == v.device == q.device and q.dtype == k.dtype == v.dtype
-    _heads(q), _heads(k), _heads(v)
-    n_q, H, hd = q.shape
-    n_kv, Hk = k.shape[0], k.shape[1]
-    assert k.shape == v.shape and k.shape[2] == hd
-    assert kv_off is not None or n_kv == n_q
-    assert kv_off is None or kv_off.numel() == q_off.numel()
+    dt, dev = q.dtype, q.get_device()
+    assert q.is_cuda and dt in _DTYPE
+    (n_q, H, hd), sq = _rows(q, "q", dt, dev)
+    k_shape, sk = _rows(k, "k", dt, dev)
+    v_shape, sv = _rows(v, "v", dt, dev)
+    n_kv, Hk, hdk = k_shape
+    assert k_shape == v_shape and hdk == hd, "k and v: other shapes than wanted"
+    qo, n = _list(q_off, "q_off", _I32, dev)
+    if kv_off is None:
+        assert n_kv == n_q, "kv_off: wanted where keys are not the queries' own tokens"
+        ko = None
+    else:
+        ko, nk = _list(kv_off, "kv_off", _I32, dev)
+        assert nk == n, "kv_off: another length than q_off"
     if out is None:
-        out = _new((n_q, H, hd), q.dtype, q.device, stream)
-    assert out.shape == q.shape and out.dtype == q.dtype and out.device == q.device
-    _heads(out)
+        out = _new((n_q, H, hd), dt, q.device, stream)
+    o_shape, so = _rows(out, "out", dt, dev)
+    assert o_shape == q.shape, "out: another shape than q"
     if scratch is None:
         scratch = attn_prompt_scratch(q, k, q_off, stream)
-    assert scratch.device == q.device and scratch.is_contiguous()
-    _launch(q.device, stream, "lt_attn_prompt", lib().lt_attn_prompt, _attn_dtype(q), _ptr(q), _row(q), _ptr(k), _row(k),
-            _ptr(v), _row(v), _ptr(out), _row(out), _off(q_off, q.device),
-            None if kv_off is None else _off(kv_off, q.device), q_off.numel() - 1, n_q, n_kv, H, Hk, hd,
-            hd ** -0.5 if scale is None else float(scale), _ptr(scratch),
-            scratch.numel() * scratch.element_size(), _status_ptr(status, q.device))
+    sc, sc_bytes = _list(scratch, "scratch", torch.uint8, dev)
+    _launch(dev, stream, "lt_attn_prompt", lib().lt_attn_prompt, _DTYPE[dt], q.data_ptr(), sq, k.data_ptr(),
+            sk, v.data_ptr(), sv, out.data_ptr(), so, qo, ko, n - 1, n_q, n_kv, H, Hk, hd,
+            hd ** -0.5 if scale is None else scale, sc, sc_bytes, _status_ptr(status, dev))
     return out
 
 
 def attn_prefix_scratch(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor,
                         stream=None) -> torch.Tensor:
-    """Scratch memory for attn_prefix calls of these sizes (or fewer rows and
-    groups), on one stream or in one captured graph at a time."""
-    need = _sz()
-    check(lib().lt_attn_prefix_scratch_bytes(_attn_dtype(q), q.shape[0], row_off.numel() - 1, q.shape[1],
-                                             cache.shape[2] // q.shape[2], q.shape[2],
-                                             ctypes.byref(need)), "lt_attn_prefix_scratch_bytes")
-    return _new(need.value, torch.uint8, q.device, stream)
+    """Scratch memory for attn_prefix calls of these sizes, on one stream or in
+    one captured graph at a time."""
+    return _scratch(lib().lt_attn_prefix_scratch_bytes, _DTYPE[q.dtype], q.device, stream, q.shape[0],
+                    row_off.numel() - 1, q.shape[1], cache.shape[2] // q.shape[2], q.shape[2])
 
 
 def attn_prefix(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor, prefix: torch.Tensor,
@@ -360,27 +362,28 @@ def attn_prefix(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor, pre
     device int32.  Group g's rows row_off[g]:row_off[g+1] attend to the slots
     prefix[prefix_off[g]:prefix_off[g+1]]; row r also to tail[tail_off[r]:tail_off[r+1]].
     Rows outside the groups keep their values in `out`.  scale: 1/sqrt(hd)."""
-    dev = q.device
-    assert q.is_cuda and cache.device == dev and q.dtype == cache.dtype
-    _heads(q)
-    n_rows, H, hd = q.shape
-    assert cache.dim() == 3 and cache.shape[1] == 2 and cache.is_contiguous()
-    assert cache.shape[2] % hd == 0
-    n_groups = row_off.numel() - 1
-    assert prefix_off.numel() == n_groups + 1 and tail_off.numel() == n_rows + 1
+    dt, dev = q.dtype, q.get_device()
+    assert q.is_cuda and dt in _DTYPE
+    (n_rows, H, hd), sq = _rows(q, "q", dt, dev)
+    (n_slots, two, width), sc_row = _rows(cache, "cache", dt, dev)
+    assert two == 2 and sc_row == 2 * width and width % hd == 0, "cache: [n_slots][2][H_kv * hd] is wanted"
+    ro, n = _list(row_off, "row_off", _I32, dev)
+    po, np_ = _list(prefix_off, "prefix_off", _I32, dev)
+    to, nt = _list(tail_off, "tail_off", _I32, dev)
+    assert np_ == n and nt == n_rows + 1, "prefix_off or tail_off: another length than wanted"
+    pre, n_prefix = _list(prefix, "prefix", _I32, dev)
+    tl, n_tail = _list(tail, "tail", _I32, dev)
     if out is None:
-        out = _new((n_rows, H, hd), q.dtype, dev, stream)
-    assert out.shape == q.shape and out.dtype == q.dtype and out.device == dev
-    _heads(out)
+        out = _new((n_rows, H, hd), dt, q.device, stream)
+    o_shape, so = _rows(out, "out", dt, dev)
+    assert o_shape == q.shape, "out: another shape than q"
     if scratch is None:
         scratch = attn_prefix_scratch(q, cache, row_off, stream)
-    assert scratch.device == dev and scratch.is_contiguous()
-    _launch(dev, stream, "lt_attn_prefix", lib().lt_attn_prefix, _attn_dtype(q), _ptr(q), _row(q), _ptr(cache),
-            cache.shape[0], _ptr(out), _row(out), _off(row_off, dev), n_groups, n_rows,
-            _list(prefix, torch.int32, dev), _off(prefix_off, dev), prefix.numel(),
-            _list(tail, torch.int32, dev), _off(tail_off, dev), tail.numel(), H, cache.shape[2] // hd,
-            hd, hd ** -0.5 if scale is None else float(scale), _ptr(scratch),
-            scratch.numel() * scratch.element_size(), _status_ptr(status, dev))
+    sc, sc_bytes = _list(scratch, "scratch", torch.uint8, dev)
+    _launch(dev, stream, "lt_attn_prefix", lib().lt_attn_prefix, _DTYPE[dt], q.data_ptr(), sq,
+            cache.data_ptr(), n_slots, out.data_ptr(), so, ro, n - 1, n_rows, pre, po, n_prefix, tl, to,
+            n_tail, H, width // hd, hd, hd ** -0.5 if scale is None else scale, sc, sc_bytes,
+            _status_ptr(status, dev))
     return out
 
 
@@ -392,22 +395,23 @@ def verify_drafts(p: torch.Tensor, q, drafts: torch.Tensor, off: torch.Tensor,
     strides, drafts int32 [n_drafts], off int32 [n + 1], uniforms fp32.  Returns
     (n_accepted int32 [n], tokens int32 [n_drafts + n]: chain s from off[s] + s on
     its accepted drafts, the drawn token, then -1)."""
-    dev = p.device
-    n, k = off.numel() - 1, drafts.numel()
-    assert p.is_cuda and p.dtype == torch.float32 and p.dim() == 2 and p.shape[0] == k + n
-    V = p.shape[1]
-    assert V == 1 or p.stride(1) == 1 or p.numel() == 0
-    if q is not None:
-        assert q.device == dev and q.dtype == torch.float32 and q.shape == (k, V)
-        assert V == 1 or q.stride(1) == 1 or k == 0
-    assert u_accept.numel() == k and u_draw.numel() == n
-    acc = _new(n, torch.int32, dev, stream)
-    tok = _new(k + n, torch.int32, dev, stream)
-    _launch(dev, stream, "lt_verify_drafts", lib().lt_verify_drafts, _ptr(p), max(_row(p), V),
-            _ptr(q) if q is not None and k else None, max(_row(q), V) if q is not None and k else V,
-            _list(drafts, torch.int32, dev), _off(off, dev), n, k, V,
-            _list(u_accept, torch.float32, dev), _list(u_draw, torch.float32, dev), _ptr(acc), _ptr(tok),
-            _status_ptr(status, dev))
+    dev = p.get_device()
+    assert p.is_cuda
+    (rows, V), sp = _rows(p, "p", _F32, dev)
+    x, k = _list(drafts, "drafts", _I32, dev)
+    of, n1 = _list(off, "off", _I32, dev)
+    ua, na = _list(u_accept, "u_accept", _F32, dev)
+    ud, nd = _list(u_draw, "u_draw", _F32, dev)
+    n = n1 - 1
+    assert rows == k + n and na == k and nd == n, "p or the uniforms: another length than wanted"
+    qp, sq = None, V
+    if q is not None and k:
+        q_shape, sq = _rows(q, "q", _F32, dev)
+        assert q_shape == (k, V), "q: another shape than wanted"
+        qp = q.data_ptr()
+    acc, tok = _new(n, _I32, p.device, stream), _new(k + n, _I32, p.device, stream)
+    _launch(dev, stream, "lt_verify_drafts", lib().lt_verify_drafts, p.data_ptr(), sp, qp, sq, x, of, n, k,
+            V, ua, ud, acc.data_ptr(), tok.data_ptr(), _status_ptr(status, dev))
     return acc, tok
 
 

@@ -193,9 +193,33 @@ inline bool attn_shape_ok(int n_heads, int n_kv_heads, int head_dim) {
   return n_kv_heads > 0 && n_kv_heads <= 1024 && n_heads > 0 && n_heads % n_kv_heads == 0 &&
          n_heads / n_kv_heads <= ATTN_MAX_GROUP;
 }
-// Lets a kernel take `bytes` of dynamic shared memory (the attribute belongs to a device).
-inline cudaError_t allow_smem(const void* kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Launches with programmatic dependence on the work before it on the stream: the kernel may start
+// while that drains, and waits for it (pdl_wait) before it reads or writes global memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid_x, unsigned grid_y, int threads, size_t smem,
+                              cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid_x, grid_y);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// Lets kernel K take `bytes` of dynamic shared memory (the attribute belongs to a device).
+template <auto K>
+inline cudaError_t allow_smem(size_t bytes) {
+  static bool set[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64 && set[dev]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev] = true;
+  return e;
 }
 // Rows start on 16-byte boundaries (vector loads and TMA).
 inline bool attn_aligned(int dtype, const void* p, long long stride) {

@@ -2,14 +2,16 @@
 //
 // A tile is (group of rows, key/value head, up to MT packed query rows); its
 // keys are the group's prefix slots followed by the tail slots of the tile's
-// own rows, in blocks of BN.  The (tile, block) units of all tiles are
-// laid end to end and CTA c of n takes units [c U / n, (c + 1) U / n),
-// so every CTA streams the same number of blocks whatever the lengths are.
-// Lengths are read on the device: a captured call follows them.
+// own rows, in blocks of BN.  Where each tile can have CTAs of its own, in
+// proportion to its blocks, a CTA takes one range of one tile (leaving a tile
+// costs a CTA a start-up and a partial: 14 us of 90 at 27.7 blocks of 512 per
+// CTA).  Otherwise the (tile, block) units of all tiles are laid end to end and
+// CTA c of n takes units [c U / n, (c + 1) U / n).  Lengths are read on the
+// device: a captured call follows them.
 //
-// CTA c's part of tile t goes to partial slot c + t: along the units either c
-// or t grows by one from a part to the next, so the slots are distinct and at
-// most grid + tiles of them are used.
+// CTA c's part of tile t goes to partial slot c + t: from a part to the next
+// one of c and t grows, so the slots are distinct and at most grid + tiles of
+// them are used.
 #pragma once
 
 #include "attn_common.cuh"
@@ -30,8 +32,7 @@ struct PrefixArgs {
   int n_groups, n_rows, n_slots, n_prefix, n_tail, heads, kv_heads, group;
   float scale;
   // scratch
-  long long* head;  // [0]: U
-  int4* tile_tab;   // per tile: first unit (x low, y high), blocks, 0
+  int4* tile_tab;   // per tile: first CTA, CTAs
   int4* row_tab;    // per row: tile of key/value head 0, tiles per head, first packed row, partials of a part
   float2* part_ml;  // [slots][MT]: maximum (log2 units) and sum
   float* part;      // [slots][MT][hd] unnormalised outputs
@@ -79,20 +80,6 @@ __device__ __forceinline__ long long warp_incl_scan(long long v) {
   return v;
 }
 
-// Units of all groups (every warp computes it alike).
-template <int BN>
-__device__ __forceinline__ long long prefix_total(const PrefixArgs& a, int tok) {
-  const int lane = threadIdx.x & 31;
-  long long n = 0;
-  for (int g = lane; g < a.n_groups; g += 32) {
-    const PrefixGroup pg = prefix_group(a, g);
-    n += (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-
 template <int BN>
 struct PrefixPos {
   PrefixGroup g;
@@ -107,50 +94,6 @@ struct PrefixPos {
     nrow = min(tok, g.m - mt * tok);
     tail = prefix_tail(a, row0, nrow);
     nb = prefix_blocks<BN>(g.np, tail.y - tail.x);
-  }
-  // The tile that holds unit u (u below the total).
-  __device__ __forceinline__ void find(const PrefixArgs& a, int tok, long long u) {
-    const int lane = threadIdx.x & 31;
-    long long base = 0, tiles = 0;
-    for (int s0 = 0; s0 < a.n_groups; s0 += 32) {
-      long long units = 0, nt = 0;
-      PrefixGroup pg = {0, 0, 0, 0};
-      int blocks = 0;
-      if (s0 + lane < a.n_groups) {
-        pg = prefix_group(a, s0 + lane);
-        blocks = prefix_group_blocks<BN>(a, pg, tok);
-        units = (long long)a.kv_heads * blocks;
-        nt = (long long)a.kv_heads * cdiv(pg.m, tok);
-      }
-      const long long iu = warp_incl_scan(units), it = warp_incl_scan(nt);
-      const unsigned here = __ballot_sync(0xffffffffu, base + iu > u);
-      if (here) {
-        const int w = __ffs(here) - 1;
-        gi = s0 + w;
-        g.r0 = __shfl_sync(0xffffffffu, pg.r0, w);
-        g.m = __shfl_sync(0xffffffffu, pg.m, w);
-        g.p0 = __shfl_sync(0xffffffffu, pg.p0, w);
-        g.np = __shfl_sync(0xffffffffu, pg.np, w);
-        blocks = __shfl_sync(0xffffffffu, blocks, w);
-        u0 = base + __shfl_sync(0xffffffffu, iu - units, w);
-        t = (int)(tiles + __shfl_sync(0xffffffffu, it - nt, w));
-        nmt = cdiv(g.m, tok);
-        kh = (int)((u - u0) / blocks);
-        u0 += (long long)kh * blocks;
-        t += kh * nmt;
-        mt = 0;
-        set_tile(a, tok);
-        while (u >= u0 + nb && mt + 1 < nmt) {
-          u0 += nb;
-          ++t;
-          ++mt;
-          set_tile(a, tok);
-        }
-        return;
-      }
-      base += __shfl_sync(0xffffffffu, iu, 31);
-      tiles += __shfl_sync(0xffffffffu, it, 31);
-    }
   }
   // The next tile (there is one: the caller still has units).
   __device__ __forceinline__ void next(const PrefixArgs& a, int tok) {
@@ -169,18 +112,6 @@ struct PrefixPos {
     }
     set_tile(a, tok);
   }
-  // Entries of the tables that the merge reads, written by the CTA with the tile's first block
-  // (threads `id` of n; `half`: rows of a 128-row half of the tile, 0 for tiles in one piece;
-  // `two`: a part of more than one block has two partials, see TcSpan).
-  __device__ __forceinline__ void publish(const PrefixArgs& a, int id, int n, int half = 0, bool two = false) const {
-    if (id == 0)
-      a.tile_tab[t] = make_int4((int)(unsigned)(u0 & 0xffffffffll), (int)(u0 >> 32), nb, 0);
-    if (kh == 0)
-      for (int i = id; i < nrow; i += n) {
-        const int r = half ? i / half * 128 + i % half * a.group : i * a.group;
-        a.row_tab[row0 + i] = make_int4(t, nmt, r, two ? 2 : 1);
-      }
-  }
 };
 
 // CTAs that get units: with fewer units than CTAs, one each (a CTA without units has no part).
@@ -192,5 +123,147 @@ __device__ __forceinline__ int prefix_cta_of(long long u, long long U, int ctas)
   while (c + 1 < ctas && prefix_u0(c + 1, U, ctas) <= u) ++c;
   return c;
 }
+
+
+// The parts of one CTA, walked through by every warp alike.
+template <int BN>
+struct PrefixWalk {
+  PrefixPos<BN> pos;
+  int b0, n;              // the part's blocks of pos's tile
+  int first_cta, n_ctas;  // the tile's CTAs
+  long long u, hi, U;     // units of this CTA, of all (units laid end to end)
+  int ctas;
+  bool own;               // the tiles have CTAs of their own
+
+  // CTAs of a tile of nb blocks that has its own.
+  __device__ __forceinline__ int share(int nb, int grid) const { return (int)max(1ll, nb * (long long)grid / U); }
+  __device__ __forceinline__ int group_share(const PrefixArgs& a, const PrefixGroup& g, int tok, int grid) const {
+    int s = 0;
+    for (int i = 0; i < g.m; i += tok) {
+      const int2 t = prefix_tail(a, g.r0 + i, min(tok, g.m - i));
+      s += share(prefix_blocks<BN>(g.np, t.y - t.x), grid);
+    }
+    return s;
+  }
+  // Sets the tile `left` shares (CTAs, or blocks where !own) into the tiles: `left` becomes what
+  // remains within the tile.  False if there is none.
+  __device__ __forceinline__ bool locate(const PrefixArgs& a, int tok, int grid, long long& left) {
+    const int lane = threadIdx.x & 31;
+    long long tiles = 0;
+    pos.u0 = 0;
+    for (int s0 = 0; s0 < a.n_groups; s0 += 32) {
+      long long sum = 0, nt = 0, blocks = 0;
+      PrefixGroup pg = {0, 0, 0, 0};
+      if (s0 + lane < a.n_groups) {
+        pg = prefix_group(a, s0 + lane);
+        blocks = (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
+        sum = own ? (long long)a.kv_heads * group_share(a, pg, tok, grid) : blocks;
+        nt = (long long)a.kv_heads * cdiv(pg.m, tok);
+      }
+      const long long is = warp_incl_scan(sum), it = warp_incl_scan(nt), ib = warp_incl_scan(blocks);
+      const unsigned here = __ballot_sync(0xffffffffu, is > left);
+      if (here) {
+        const int w = __ffs(here) - 1;
+        pos.gi = s0 + w;
+        pos.g.r0 = __shfl_sync(0xffffffffu, pg.r0, w);
+        pos.g.m = __shfl_sync(0xffffffffu, pg.m, w);
+        pos.g.p0 = __shfl_sync(0xffffffffu, pg.p0, w);
+        pos.g.np = __shfl_sync(0xffffffffu, pg.np, w);
+        left -= __shfl_sync(0xffffffffu, is - sum, w);
+        pos.u0 += __shfl_sync(0xffffffffu, ib - blocks, w);
+        pos.t = (int)(tiles + __shfl_sync(0xffffffffu, it - nt, w));
+        const long long per = __shfl_sync(0xffffffffu, sum, w) / a.kv_heads;  // of one head
+        pos.nmt = cdiv(pos.g.m, tok);
+        pos.kh = (int)(left / per);
+        left -= pos.kh * per;
+        pos.t += pos.kh * pos.nmt;
+        pos.u0 += pos.kh * (__shfl_sync(0xffffffffu, blocks, w) / a.kv_heads);
+        for (pos.mt = 0;; ++pos.mt) {
+          pos.set_tile(a, tok);
+          const int here_n = own ? share(pos.nb, grid) : pos.nb;
+          if (left < here_n || pos.mt + 1 >= pos.nmt) break;
+          left -= here_n;
+          pos.u0 += pos.nb;
+          ++pos.t;
+        }
+        return true;
+      }
+      left -= __shfl_sync(0xffffffffu, is, 31);
+      pos.u0 += __shfl_sync(0xffffffffu, ib, 31);
+      tiles += __shfl_sync(0xffffffffu, it, 31);
+    }
+    return false;
+  }
+  __device__ __forceinline__ void set_part() {
+    b0 = (int)(u - pos.u0);
+    n = (int)min((long long)pos.nb - b0, hi - u);
+    first_cta = prefix_cta_of(pos.u0, U, ctas);
+    n_ctas = prefix_cta_of(pos.u0 + pos.nb - 1, U, ctas) - first_cta + 1;
+  }
+  // The first part of CTA `cta` of `grid`; false: it has none.
+  __device__ __forceinline__ bool start(const PrefixArgs& a, int tok, int cta, int grid) {
+    const int lane = threadIdx.x & 31;
+    long long units = 0, tiles = 0;
+    for (int g = lane; g < a.n_groups; g += 32) {
+      const PrefixGroup pg = prefix_group(a, g);
+      units += (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
+      tiles += (long long)a.kv_heads * cdiv(pg.m, tok);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      units += __shfl_xor_sync(0xffffffffu, units, o);
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+    }
+    U = units;
+    if (U == 0) return false;
+    // CTAs of their own: at least two per tile on average and fewer than a block would make idle
+    own = 2 * tiles <= grid && U >= grid;
+    if (own) {
+      long long shares = 0;
+      for (int g = lane; g < a.n_groups; g += 32)
+        shares += (long long)a.kv_heads * group_share(a, prefix_group(a, g), tok, grid);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) shares += __shfl_xor_sync(0xffffffffu, shares, o);
+      own = shares <= grid;
+    }
+    if (own) {
+      long long k = cta;
+      if (!locate(a, tok, grid, k)) return false;
+      n_ctas = share(pos.nb, grid);
+      first_cta = cta - (int)k;
+      b0 = (int)(k * pos.nb / n_ctas);
+      n = (int)((k + 1) * pos.nb / n_ctas) - b0;
+      return true;
+    }
+    ctas = prefix_ctas(U, grid);
+    if (cta >= ctas) return false;
+    u = prefix_u0(cta, U, ctas);
+    hi = prefix_u0(cta + 1, U, ctas);
+    long long left = u;
+    if (!locate(a, tok, grid, left)) return false;
+    set_part();
+    return true;
+  }
+  // The next part; false: there is none.
+  __device__ __forceinline__ bool next(const PrefixArgs& a, int tok) {
+    if (own || (u += n) >= hi) return false;
+    pos.next(a, tok);
+    set_part();
+    return true;
+  }
+  // Entries of the tables that the merge reads, written with the tile's first block (threads `id` of
+  // `threads`; `half`: rows of a 128-row half of the tile, 0 for tiles in one piece; `two`: a part has
+  // two partials, see TcSpan).
+  __device__ __forceinline__ void publish(const PrefixArgs& a, int id, int threads, int half = 0,
+                                          bool two = false) const {
+    if (b0 != 0) return;
+    if (id == 0) a.tile_tab[pos.t] = make_int4(first_cta, n_ctas, 0, 0);
+    if (pos.kh == 0)
+      for (int i = id; i < pos.nrow; i += threads) {
+        const int r = half ? i / half * 128 + i % half * a.group : i * a.group;
+        a.row_tab[pos.row0 + i] = make_int4(pos.t, pos.nmt, r, two ? 2 : 1);
+      }
+  }
+};
 
 }  // namespace lt

@@ -59,22 +59,19 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
   const int gr = lane >> 2, gc = (lane & 3) * 2;
   const uint32_t smem = smem_u32(smem_raw);
   const int group = a.group, tok = MT / group;
-  const long long U = prefix_total<PREFIX_N>(a, tok);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = U;
-  const int ctas = prefix_ctas(U, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
+  pdl_trigger();
+  PrefixWalk<PREFIX_N> walk;
+  if (!walk.start(a, tok, blockIdx.x, gridDim.x)) return;
+  const PrefixPos<PREFIX_N>& pos = walk.pos;
   const size_t width = (size_t)a.kv_heads * HD;
   const float sl = a.scale * 1.4426950408889634f;  // scores in log2 units
-  PrefixPos<PREFIX_N> pos;
-  pos.find(a, tok, lo);
-  for (long long u = lo; u < hi;) {
+  do {
     if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
       set_err(a.status, DEV_BAD_INDEX);
       return;
     }
-    if (u == pos.u0) pos.publish(a, threadIdx.x, C::THREADS);
-    const int b0 = (int)(u - pos.u0), b1 = (int)min((long long)pos.nb, b0 + (hi - u));
+    walk.publish(a, threadIdx.x, C::THREADS);
+    const int b0 = walk.b0, b1 = b0 + walk.n;
     const int rows = pos.nrow * group;
     const int np = pos.g.np, nk = np + pos.tail.y - pos.tail.x;
     const __nv_bfloat16* kc = (const __nv_bfloat16*)a.cache + (size_t)pos.kh * HD;
@@ -308,9 +305,7 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
         *reinterpret_cast<float4*>(a.part + (part * MT + r) * HD + c) = acc;
       }
     }
-    u += b1 - b0;
-    if (u < hi) pos.next(a, tok);
-  }
+  } while (walk.next(a, tok));
 }
 
 }  // namespace lt

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.group, tok = 128 / group;
-  pdl_trigger();  // the join may be launched: it waits for this grid's end before it reads
+  pdl_trigger();  // what follows may be launched: it waits for this grid's end before it reads
 
   const uint32_t q_s = smem_u32(smem_raw), ring = q_s + 2 * C::TILE;
   const uint32_t q_full = smem_u32(&sb.q_full), q_empty = smem_u32(&sb.q_empty), fin = smem_u32(&sb.fin);
@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem = sb.tmem;
   auto s_col = [&](int t) { return tmem + (uint32_t)t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + (uint32_t)t * C::OCOLS; };
@@ -546,29 +547,22 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       };
       if constexpr (GATHER) {
         const int rows = 2 * tok;  // of a pair of tiles
-        const long long U = prefix_total<128>(a, rows);
-        if (blockIdx.x == 0 && lane == 0) a.head[0] = U;
-        const int ctas = prefix_ctas(U, gridDim.x);
         int it = 0;
-        if (blockIdx.x < ctas) {
-          const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
-          PrefixPos<128> pos;
-          pos.find(a, rows, lo);
-          for (long long u = lo; u < hi;) {
+        PrefixWalk<128> walk;
+        if (walk.start(a, rows, blockIdx.x, gridDim.x)) {
+          do {
+            const PrefixPos<128>& pos = walk.pos;
             if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
               set_err(a.status, DEV_BAD_INDEX);
               break;
             }
-            if (u == pos.u0) pos.publish(a, lane, 32, tok, pos.nrow <= tok);
-            const int b0 = (int)(u - pos.u0), n = (int)min((long long)pos.nb - b0, hi - u);
+            walk.publish(a, lane, 32, tok, pos.nrow <= tok);
             if (!hand_over(it, PrefixItem{pos.row0, pos.nrow, pos.g.p0, pos.g.np, pos.tail.x,
-                                          pos.g.np + pos.tail.y - pos.tail.x, b0, n, 0, pos.kh,
+                                          pos.g.np + pos.tail.y - pos.tail.x, walk.b0, walk.n, 0, pos.kh,
                                           (int)blockIdx.x + pos.t}))
               break;
             ++it;
-            u += n;
-            if (u < hi) pos.next(a, rows);
-          }
+          } while (walk.next(a, rows));
         }
         hand_over(it, PrefixItem{0, 0, 0, 0, 0, 0, 0, 0, -1, 0, 0});
       } else {
@@ -776,6 +770,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       turns += most;
       if (!ok) break;
       const bool partial = W::partial(a);
+      if (GATHER && nb == 0 && valid) a.part_ml[(size_t)item.part * 256 + t * 128 + r] = make_float2(-INFINITY, 0.f);
       if (nt > 0 && (nb > 0 || !partial)) {
         if (nb > 0) {
           if (!(ok = wait(o_done(t), (done + nb - 1) & 1))) break;

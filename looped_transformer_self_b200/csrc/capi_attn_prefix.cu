@@ -3,7 +3,6 @@
 // of one committed prefix, or the samples of one prompt), and each row's own
 // tail is read for it alone.
 #include "../../include/looped_spec.h"
-#include <stdlib.h>
 #include "attn_prefix_mma.cuh"
 
 namespace lt {
@@ -15,22 +14,20 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
   SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
   __shared__ int slot[PREFIX_N];
   const int tok = SIMT_M / a.group, group = a.group;
-  const long long U = prefix_total<PREFIX_N>(a, tok);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.head[0] = U;
-  const int ctas = prefix_ctas(U, gridDim.x);
-  if (blockIdx.x >= ctas) return;
-  const long long lo = prefix_u0(blockIdx.x, U, ctas), hi = prefix_u0(blockIdx.x + 1, U, ctas);
+  pdl_trigger();
+  pdl_wait();
+  PrefixWalk<PREFIX_N> walk;
+  if (!walk.start(a, tok, blockIdx.x, gridDim.x)) return;
+  const PrefixPos<PREFIX_N>& pos = walk.pos;
   const size_t width = (size_t)a.kv_heads * HD;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  PrefixPos<PREFIX_N> pos;
-  pos.find(a, tok, lo);
-  for (long long u = lo; u < hi;) {
+  do {
     if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
       set_err(a.status, DEV_BAD_INDEX);
       return;
     }
-    if (u == pos.u0) pos.publish(a, threadIdx.x, SIMT_THREADS);
-    const int b0 = (int)(u - pos.u0), b1 = (int)min((long long)pos.nb, b0 + (hi - u));
+    walk.publish(a, threadIdx.x, SIMT_THREADS);
+    const int b0 = walk.b0, b1 = b0 + walk.n;
     const int rows = pos.nrow * group, h0 = pos.kh * group;
     const T* q = (const T*)a.q + (size_t)pos.row0 * a.sq + (size_t)h0 * HD;
     __syncthreads();  // the previous tile's queries are consumed
@@ -82,9 +79,7 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
       for (int c = 0; c < HD / 32; ++c)
         *reinterpret_cast<float2*>(o + tx * 2 + 32 * c) = make_float2(st.o[i][2 * c], st.o[i][2 * c + 1]);
     }
-    u += b1 - b0;
-    if (u < hi) pos.next(a, tok);
-  }
+  } while (walk.next(a, tok));
 }
 
 // Merge of a row's partials: with M the largest m, o = sum_i 2^(m_i - M) O_i /
@@ -98,35 +93,29 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   // rows before the first group or behind the last one are left as they were
   const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
   if (row < first || row >= last) return;
-  const long long U = a.head[0];
   const int4 rt = a.row_tab[row];
   const int t = rt.x + (h / a.group) * rt.y, r = rt.z + h % a.group;
-  if (U <= 0 || t < 0 || t >= a.max_tiles || r < 0 || r >= MT) {  // rows that the offsets do not reach
+  if (t < 0 || t >= a.max_tiles || r < 0 || r >= MT) {  // rows that the offsets do not reach
     set_err(a.status, DEV_BAD_INDEX);
     return;
   }
   const int4 tt = a.tile_tab[t];
-  const long long u0 = (long long)(unsigned)tt.x | ((long long)tt.y << 32);
-  if (u0 < 0 || tt.z <= 0 || u0 + tt.z > U) {
+  if (tt.x < 0 || tt.y <= 0 || tt.x + tt.y > grid) {
     set_err(a.status, DEV_BAD_INDEX);
     return;
   }
-  const int ctas = prefix_ctas(U, grid);
-  const long long u1 = u0 + tt.z;
-  const int c0 = prefix_cta_of(u0, U, ctas), c1 = prefix_cta_of(u1 - 1, U, ctas), two = rt.w == 2 ? 2 : 1;
+  const int two = rt.w == 2 ? 2 : 1, parts = tt.y * two;
   float M = -INFINITY, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   constexpr int B = 8;  // partials in flight
-  for (int k0 = 0; k0 < (c1 - c0 + 1) * two; k0 += B) {
+  for (int k0 = 0; k0 < parts; k0 += B) {
     float2 ml[B];
     float v[B][PER];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int c = c0 + (k0 + k) / two, e = (k0 + k) % two;
-      // the second partial of a part of one block is not there
-      const bool there = c <= c1 && (e == 0 || min(u1, prefix_u0(c + 1, U, ctas)) - max(u0, prefix_u0(c, U, ctas)) > 1);
-      const size_t p = (size_t)(c + t) * MT + e * (MT / 2) + r;
+      const bool there = k0 + k < parts;
+      const size_t p = (size_t)(tt.x + (k0 + k) / two + t) * MT + (k0 + k) % two * (MT / 2) + r;
       ml[k] = there ? a.part_ml[p] : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[k][i] = there ? a.part[p * HD + lane * PER + i] : 0.f;
@@ -141,6 +130,7 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
     for (int i = 0; i < PER; ++i) o[i] *= f;
 #pragma unroll
     for (int k = 0; k < B; ++k) {
+      if (ml[k].x == -INFINITY) continue;  // a partial that saw nothing has no outputs
       const float w = ex2(ml[k].x - ms);
       l += w * ml[k].y;
 #pragma unroll
@@ -155,30 +145,22 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
 
 template <typename T, int HD, int MT>
 static cudaError_t prefix_merge(const PrefixArgs& a, int grid, cudaStream_t st) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_rows, cdiv(a.heads, 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_prefix_merge<T, HD, MT>, a, grid);
+  return launch_pdl(k_attn_prefix_merge<T, HD, MT>, a.n_rows, cdiv(a.heads, 8), 256, 0, st, a, grid);
 }
 
 template <int HD>
 static cudaError_t prefix_f32(const PrefixArgs& a, int grid, cudaStream_t st) {
-  if (cudaError_t e = allow_smem((const void*)k_attn_prefix_simt<float, HD>, sizeof(SimtSmem<HD>))) return e;
-  k_attn_prefix_simt<float, HD><<<grid, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
+  if (cudaError_t e = allow_smem<k_attn_prefix_simt<float, HD>>(sizeof(SimtSmem<HD>))) return e;
+  if (cudaError_t e = launch_pdl(k_attn_prefix_simt<float, HD>, grid, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a))
+    return e;
   return prefix_merge<float, HD, SIMT_M>(a, grid, st);
 }
 
 template <int HD, int MT>
 static cudaError_t prefix_mma(const PrefixArgs& a, int grid, cudaStream_t st) {
   using C = PrefixMma<HD, MT>;
-  if (cudaError_t e = allow_smem((const void*)k_attn_prefix_mma<HD, MT>, C::SMEM)) return e;
-  k_attn_prefix_mma<HD, MT><<<grid, C::THREADS, C::SMEM, st>>>(a);
+  if (cudaError_t e = allow_smem<k_attn_prefix_mma<HD, MT>>(C::SMEM)) return e;
+  if (cudaError_t e = launch_pdl(k_attn_prefix_mma<HD, MT>, grid, 1, C::THREADS, C::SMEM, st, a)) return e;
   return prefix_merge<__nv_bfloat16, HD, MT>(a, grid, st);
 }
 
@@ -187,8 +169,8 @@ static cudaError_t prefix_tc(const PrefixArgs& a, int grid, cudaStream_t st) {
   using W = PrefixWork;
   CUtensorMap mq;
   if (attn_tmap(&mq, a.q, HD, a.heads, a.n_rows, a.sq, a.group, 128 / a.group)) return cudaErrorInvalidValue;
-  if (cudaError_t e = allow_smem((const void*)k_attn_tc<HD, W>, tc_smem<HD, W>())) return e;
-  k_attn_tc<HD, W><<<grid, W::THREADS, tc_smem<HD, W>(), st>>>(a, mq, mq, mq);
+  if (cudaError_t e = allow_smem<k_attn_tc<HD, W>>(tc_smem<HD, W>())) return e;
+  if (cudaError_t e = launch_pdl(k_attn_tc<HD, W>, grid, 1, W::THREADS, tc_smem<HD, W>(), st, a, mq, mq, mq)) return e;
   return prefix_merge<__nv_bfloat16, HD, 256>(a, grid, st);
 }
 
@@ -203,33 +185,40 @@ static cudaError_t prefix_any(int dtype, int mt, const PrefixArgs& a, int grid, 
   }
 }
 
-// Scratch layout: total, tile table, row table, (m, l) pairs, partial outputs.
+// Scratch layout: tile table, row table, (m, l) pairs, partial outputs.
 struct PrefixPlan {
   int mt, grid;
   long long max_tiles;
-  size_t tile_at, row_at, ml_at, part_at, bytes;
+  size_t row_at, ml_at, part_at, bytes;
 };
-static PrefixPlan prefix_plan(int dtype, int n_rows, int n_groups, int n_heads, int n_kv_heads, int hd) {
+static PrefixPlan prefix_plan(int mt, int n_rows, int n_groups, int n_heads, int n_kv_heads, int hd) {
   PrefixPlan p;
-  const int group = n_heads / n_kv_heads;
-  p.mt = SIMT_M;
-  if (dtype == LT_BF16) {
-    // the smallest tile that holds an average group's packed rows (a group may take several tiles)
-    const long long avg = (long long)group * n_rows / (n_groups > 0 ? n_groups : 1);
-    p.mt = avg <= 16 && group <= 16 ? 16 : avg <= 32 && group <= 32 ? 32 : 64;
-    if (getenv("KIND") && atoi(getenv("KIND"))) p.mt = 256;
-  }
-  const int tok = p.mt == 256 ? 2 * (128 / group) : p.mt / group;
-  p.grid = (p.mt == 256 ? 1 : 2) * attn_sm_count();
+  const int group = n_heads / n_kv_heads, tok = mt == 256 ? 2 * (128 / group) : mt / group;
+  p.mt = mt;
+  p.grid = (mt == 256 ? 1 : 2) * attn_sm_count();
   p.max_tiles = (long long)n_kv_heads * (n_rows / tok + (long long)n_groups);
   const size_t slots = (size_t)p.max_tiles + p.grid;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  p.tile_at = 256;
-  p.row_at = p.tile_at + up((size_t)p.max_tiles * sizeof(int4));
+  p.row_at = up((size_t)p.max_tiles * sizeof(int4));
   p.ml_at = p.row_at + up((size_t)n_rows * sizeof(int4));
-  p.part_at = p.ml_at + up(slots * p.mt * sizeof(float2));
-  p.bytes = p.part_at + up(slots * p.mt * (size_t)hd * sizeof(float));
+  p.part_at = p.ml_at + up(slots * mt * sizeof(float2));
+  p.bytes = p.part_at + up(slots * mt * (size_t)hd * sizeof(float));
   return p;
+}
+// The smallest tile of the few-rows kernels that holds an average group's packed rows (a group may
+// take several tiles).
+static int prefix_small_tile(int dtype, int n_rows, int n_groups, int group) {
+  const long long avg = (long long)group * n_rows / (n_groups > 0 ? n_groups : 1);
+  if (dtype == LT_F32) return SIMT_M;
+  return avg <= 16 && group <= 16 ? 16 : avg <= 32 && group <= 32 ? 32 : 64;
+}
+// The tensor-core tiles (256 packed rows) cost about 4 us more to start and less per key; the more
+// rows the few-rows kernel holds, the fewer keys it takes to make that up.  Measured at head size 128
+// (few rows / tiles): 16 heads, 1 row, 6000 keys 26.2 / 28.1 us, 20000 keys 48.8 / 45.3; 32 rows,
+// 1000 keys 15.3 / 18.1, 2500 keys 23.7 / 22.9, 20000 keys 58.7 / 45.8; 32 heads on 8, 32 rows, 2500
+// keys 28.0 / 25.6, 20000 keys 75.3 / 42.4.
+static bool prefix_use_tc(int mt, long long keys, int n_kv_heads) {
+  return keys * n_kv_heads >= (mt == 64 ? 24000 : mt == 32 ? 48000 : 160000);
 }
 
 }  // namespace lt
@@ -240,9 +229,14 @@ extern "C" int lt_attn_prefix_scratch_bytes(int dtype, int n_rows, int n_groups,
                                             int n_kv_heads, int head_dim, size_t* bytes) {
   if (!bytes || (dtype != LT_F32 && dtype != LT_BF16) || n_rows < 0 || n_groups < 0) return LT_ERR_ARG;
   if (!attn_shape_ok(n_heads, n_kv_heads, head_dim) || n_rows > 65535) return LT_ERR_SHAPE;
-  const PrefixPlan p = prefix_plan(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
+  const int small = prefix_small_tile(dtype, n_rows, n_groups, n_heads / n_kv_heads);
+  const PrefixPlan p = prefix_plan(small, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
   if (p.max_tiles > (1 << 30)) return LT_ERR_SHAPE;
   *bytes = p.bytes;
+  if (dtype == LT_BF16) {  // either kernel may run: the number of keys decides
+    const size_t tc = prefix_plan(256, n_rows, n_groups, n_heads, n_kv_heads, head_dim).bytes;
+    if (tc > *bytes) *bytes = tc;
+  }
   return LT_OK;
 }
 
@@ -267,11 +261,13 @@ extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, co
       ((uintptr_t)d_cache & 15) || ((uintptr_t)d_scratch & 15))
     return LT_ERR_SHAPE;
   if (scratch_bytes < need) return LT_ERR_CAPACITY;
-  const PrefixPlan p = prefix_plan(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
+  int mt = prefix_small_tile(dtype, n_rows, n_groups, n_heads / n_kv_heads);
+  if (dtype == LT_BF16 && prefix_use_tc(mt, (long long)n_prefix + n_tail, n_kv_heads)) mt = 256;
+  const PrefixPlan p = prefix_plan(mt, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
   char* s = (char*)d_scratch;
   PrefixArgs a = {d_q, d_cache, d_o, stride_q, stride_o, d_row_off, d_prefix, d_prefix_off, d_tail,
                   d_tail_off, n_groups, n_rows, n_slots, n_prefix, n_tail, n_heads, n_kv_heads,
-                  n_heads / n_kv_heads, scale, (long long*)s, (int4*)(s + p.tile_at),
+                  n_heads / n_kv_heads, scale, (int4*)s,
                   (int4*)(s + p.row_at), (float2*)(s + p.ml_at), (float*)(s + p.part_at),
                   (int)p.max_tiles, d_status};
   cudaStream_t st = (cudaStream_t)stream;

@@ -13,6 +13,8 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prompt_simt(PromptArgs
   extern __shared__ __align__(16) char smem_raw[];
   SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
   const int kh = blockIdx.x % a.kv_heads, tok = SIMT_M / a.group;
+  pdl_trigger();
+  pdl_wait();
   PromptTile pt;
   if (!prompt_tile(a, blockIdx.x / a.kv_heads, tok, pt)) return;
   const int t0 = pt.tile * tok, nt = min(tok, pt.lq - t0), rows = nt * a.group;
@@ -53,9 +55,8 @@ template <typename T, int HD>
 static cudaError_t prompt_simt(const PromptArgs& a, cudaStream_t st) {
   const int tok = SIMT_M / a.group;
   const unsigned tiles = (unsigned)(a.n_q / tok + a.n_seqs);
-  if (cudaError_t e = allow_smem((const void*)k_attn_prompt_simt<T, HD>, sizeof(SimtSmem<HD>))) return e;
-  k_attn_prompt_simt<T, HD><<<tiles * a.kv_heads, SIMT_THREADS, sizeof(SimtSmem<HD>), st>>>(a);
-  return cudaGetLastError();
+  if (cudaError_t e = allow_smem<k_attn_prompt_simt<T, HD>>(sizeof(SimtSmem<HD>))) return e;
+  return launch_pdl(k_attn_prompt_simt<T, HD>, tiles * a.kv_heads, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a);
 }
 
 template <int HD>
@@ -70,23 +71,15 @@ static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
   if (attn_tmap(&mq, a.q, HD, a.heads, a.n_q, a.sq, a.group, tok) ||
       attn_tmap(&mk, k, HD, a.kv_heads, nk, a.sk, 1, 128) || attn_tmap(&mv, v, HD, a.kv_heads, nk, a.sv, 1, 128))
     return LT_ERR_CUDA;
-  if (allow_smem((const void*)k_attn_tc<HD, W>, tc_smem<HD, W>()) != cudaSuccess) return LT_ERR_CUDA;
+  if (allow_smem<k_attn_tc<HD, W>>(tc_smem<HD, W>()) != cudaSuccess) return LT_ERR_CUDA;
   const unsigned pairs = (unsigned)prompt_pairs(a.n_q, a.n_seqs, a.group) * a.kv_heads;
-  k_attn_tc<HD, W><<<pairs * a.splits, W::THREADS, tc_smem<HD, W>(), st>>>(a, mq, mk, mv);
+  if (launch_pdl(k_attn_tc<HD, W>, pairs * a.splits, 1, W::THREADS, tc_smem<HD, W>(), st, a, mq, mk, mv) != cudaSuccess)
+    return LT_ERR_CUDA;
   if (a.splits > 1) {
-    cudaLaunchConfig_t cfg = {};
     const int parts = cdiv(256, prompt_join_rows<HD>());
-    cfg.gridDim = dim3(pairs * parts);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, k_attn_prompt_join<HD>, a, parts) != cudaSuccess) return LT_ERR_CUDA;
+    if (launch_pdl(k_attn_prompt_join<HD>, pairs * parts, 1, 256, 0, st, a, parts) != cudaSuccess) return LT_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+  return LT_OK;
 }
 
 template <int HD>

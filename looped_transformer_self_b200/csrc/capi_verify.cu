@@ -5,13 +5,13 @@
 #include <cooperative_groups.h>
 
 #include "../../include/looped_spec.h"
-#include "common.cuh"
+#include "attn_common.cuh"
 
 namespace lt {
 
 namespace cg = cooperative_groups;
 
-constexpr int VERIFY_THREADS = 512, VERIFY_WARPS = VERIFY_THREADS / 32;
+constexpr int VERIFY_THREADS = 256, VERIFY_WARPS = VERIFY_THREADS / 32;
 constexpr int VERIFY_SEG = 512;      // vocabulary entries one warp sums at a time
 constexpr int VERIFY_MAX_SEGS = 256; // segments of one CTA whose sums are kept
 
@@ -132,7 +132,7 @@ __device__ __forceinline__ int seg_pick(const float w[16], int base, double befo
 // Bound by HBM for a batch (one row of p and one of q per sequence) and by the
 // chain of dependent loads for one sequence.
 template <bool VEC>
-__global__ void __launch_bounds__(VERIFY_THREADS) k_verify(VerifyArgs a, int seg_units) {
+__global__ void __launch_bounds__(VERIFY_THREADS, 4) k_verify(VerifyArgs a, int seg_units) {
   __shared__ double seg_sum[VERIFY_MAX_SEGS];
   __shared__ double total;
   __shared__ double run_at;
@@ -140,6 +140,8 @@ __global__ void __launch_bounds__(VERIFY_THREADS) k_verify(VerifyArgs a, int seg
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int s = blockIdx.x / nr, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  pdl_trigger();
+  pdl_wait();
   const int o0 = __ldg(a.off + s), o1 = __ldg(a.off + s + 1);
   const bool bad = o0 < 0 || o1 < o0 || o1 > a.n_drafts;  // the same in every CTA of the cluster
   if (bad) {
@@ -290,10 +292,11 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
   if (!d_p || !d_off || !d_u_draw || !d_n_accepted || !d_tokens || stride_p < V ||
       (n_drafts > 0 && (!d_draft || !d_u_accept)) || (d_q && stride_q < V))
     return LT_ERR_ARG;
-  // Eight CTAs a sequence while the batch leaves SMs free (latency), fewer for large batches or
-  // short rows (a CTA sums VERIFY_WARPS segments at a time).
+  // Eight CTAs a sequence for latency (one chain at a vocabulary of 49152: 7.1 us, 18.2 us with one),
+  // fewer where all of them would not be resident at once (192 chains at 65536: 26.7 us with two,
+  // 33.2 us with eight) or would have less than a segment per warp.
   int nr = 8;
-  while (nr > 1 && ((long long)n_seqs * nr > 1184 || (long long)(nr / 2) * VERIFY_WARPS * VERIFY_SEG >= V)) nr /= 2;
+  while (nr > 1 && ((long long)n_seqs * nr > 4ll * attn_sm_count() || (long long)(nr / 2) * VERIFY_WARPS * VERIFY_SEG >= V)) nr /= 2;
   const long long segs = ((long long)V + VERIFY_SEG - 1) / VERIFY_SEG;
   const int units = (int)((segs + (long long)nr * VERIFY_MAX_SEGS - 1) / ((long long)nr * VERIFY_MAX_SEGS));
   VerifyArgs a = {d_p, d_q, stride_p, stride_q, d_draft, d_off, n_seqs, n_drafts, V, d_u_accept,
@@ -304,12 +307,14 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
   cfg.gridDim = dim3((unsigned)(n_seqs * (long long)nr));
   cfg.blockDim = dim3(VERIFY_THREADS);
   cfg.stream = (cudaStream_t)stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = nr;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, k_verify<true>, a, units)
                             : cudaLaunchKernelEx(&cfg, k_verify<false>, a, units);
   return e == cudaSuccess ? LT_OK : LT_ERR_CUDA;
