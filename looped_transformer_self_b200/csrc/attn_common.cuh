@@ -31,29 +31,20 @@ __device__ __forceinline__ int2 off_range(const int32_t* __restrict__ off, int i
 // a block of scores s gives m' = max(m, max s), p = exp(s - m'),
 // l' = l exp(m - m') + sum p, O' = O exp(m - m') + p V.  Thread (ty, tx) of a
 // 16 x 16 grid holds scores of rows 4 ty + i and keys tx + 16 j, and output
-// columns 2 tx + 32 c.  K and V share one buffer, so two CTAs fit an SM.
+// columns 2 tx + 32 c.  A block's keys are copied while the block before is
+// multiplied with its values and its values during its scores (cp.async); at
+// head size 128 the four arrays are just half of an SM's shared memory, so two
+// CTAs fit.
 constexpr int SIMT_M = 64, SIMT_N = 64, SIMT_THREADS = 256;
 
 template <int HD>
 struct SimtSmem {
-  float q[SIMT_M][HD + 4];
-  float kv[SIMT_N][HD + 4];  // pitch HD + 4: eight rows read as float4 touch all banks once
-  float p[SIMT_M][SIMT_N + 4];
+  float k[SIMT_N][HD + 4];  // pitch HD + 4: eight rows read as float4 touch all banks once
+  float q[SIMT_M][HD];
+  float v[SIMT_N][HD];
+  float p[SIMT_M][SIMT_N];  // column c of row r at c ^ 16 (r / 4 % 2): a warp's two row groups in different banks
 };
-
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-  return *reinterpret_cast<const float4*>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  return make_float4(a.x, a.y, b.x, b.y);
-}
+__device__ __forceinline__ int simt_p_col(int r, int c) { return c ^ ((r >> 2 & 1) << 4); }
 
 // Row state of one tile: 4 rows per thread, replicated over the 16 threads of a row.
 template <int HD>
@@ -71,16 +62,31 @@ struct SimtState {
 };
 
 // Copies the tile's query rows (scaled) to shared memory; rows without a pointer are zero.
-template <typename T, int HD, typename RowPtr>
+template <int HD, typename RowPtr>
 __device__ __forceinline__ void simt_load_q(SimtSmem<HD>& sm, RowPtr row, float scale) {
   for (int e = threadIdx.x; e < SIMT_M * (HD / 4); e += SIMT_THREADS) {
     const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
-    const T* p = row(r);
-    float4 v = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* p = row(r);
+    float4 v = p ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     v.x *= scale; v.y *= scale; v.z *= scale; v.w *= scale;
     *reinterpret_cast<float4*>(&sm.q[r][c]) = v;
   }
 }
+// Starts the copy of 64 rows (a copy group of its own); rows without a pointer become zero.  `any`:
+// a valid address, not read for those.
+template <int HD, int PITCH, typename RowPtr>
+__device__ __forceinline__ void simt_fetch(float* dst, RowPtr row, const float* any) {
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+  for (int e = threadIdx.x; e < SIMT_N * (HD / 4); e += SIMT_THREADS) {
+    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
+    const float* p = row(r);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (r * PITCH + c) * 4),
+                 "l"(p ? p + c : any), "r"(p ? 16 : 0)
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void simt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void simt_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
 // O += P V of one block.  GUARD: a weight of 0 takes nothing from its value
 // row, so that an infinity or NaN in a key that the row does not see stays
@@ -92,12 +98,13 @@ __device__ __forceinline__ void simt_pv(SimtSmem<HD>& sm, SimtState<HD>& st) {
   for (int k = 0; k < SIMT_N; k += 4) {
     float4 p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.p[ty * 4 + i][k]);
+    for (int i = 0; i < 4; ++i)
+      p[i] = *reinterpret_cast<const float4*>(&sm.p[ty * 4 + i][simt_p_col(ty * 4, k)]);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) {
-        const float2 v = *reinterpret_cast<const float2*>(&sm.kv[k + u][tx * 2 + 32 * c]);
+        const float2 v = *reinterpret_cast<const float2*>(&sm.v[k + u][tx * 2 + 32 * c]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
@@ -109,20 +116,16 @@ __device__ __forceinline__ void simt_pv(SimtSmem<HD>& sm, SimtState<HD>& st) {
   }
 }
 
-// One block of 64 keys: `key(j)` / `val(j)` give key j's rows or nullptr (a key
-// that no row sees: its value is zero, so that nothing of it reaches a row),
-// `seen(r, j)` whether packed row r sees key j; `masked` (uniform): some row may
-// not see some key of the block.
-template <typename T, int HD, typename KeyPtr, typename ValPtr, typename Seen>
-__device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, KeyPtr key, ValPtr val,
-                                           Seen seen, bool masked) {
+// One block of 64 keys whose copies were started as the group before last (keys) and the last
+// (values).  `seen(r, j)` says whether packed row r sees key j; `masked` (uniform): some row may not
+// see some key of the block.  next_k() / next_v() start the next block's copies, a group each (empty
+// at the end), where their buffers are free; before_k() runs between the scores and next_k, with a
+// barrier on both sides.
+template <int HD, typename Seen, typename Before, typename NextK, typename NextV>
+__device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, Seen seen, bool masked,
+                                           Before before_k, NextK next_k, NextV next_v) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  __syncthreads();  // the previous block's V (and P) is consumed
-  for (int e = threadIdx.x; e < SIMT_N * (HD / 4); e += SIMT_THREADS) {
-    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
-    const T* p = key(r);
-    *reinterpret_cast<float4*>(&sm.kv[r][c]) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
+  simt_wait1();
   __syncthreads();
   float s[4][4];
 #pragma unroll
@@ -135,7 +138,7 @@ __device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][d]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.kv[tx + 16 * j][d]);
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][d]);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -147,14 +150,18 @@ __device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, 
       }
   }
 #pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (!seen(ty * 4 + i, tx + 16 * j)) s[i][j] = -INFINITY;
+  before_k();
+  __syncthreads();  // the keys are consumed
+  next_k();
+  simt_commit();
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = ty * 4 + i;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (!seen(r, tx + 16 * j)) s[i][j] = -INFINITY;
-      mx = fmaxf(mx, s[i][j]);
-    }
+    float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float mn = fmaxf(st.m[i], mx);
@@ -165,7 +172,7 @@ __device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, 
     for (int j = 0; j < 4; ++j) {
       const float p = expf(s[i][j] - ms);
       sum += p;
-      sm.p[r][tx + 16 * j] = p;
+      sm.p[r][simt_p_col(r, tx + 16 * j)] = p;
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -174,17 +181,15 @@ __device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, 
 #pragma unroll
     for (int c = 0; c < HD / 16; ++c) st.o[i][c] *= f;
   }
-  __syncthreads();  // P is complete and K consumed
-  for (int e = threadIdx.x; e < SIMT_N * (HD / 4); e += SIMT_THREADS) {
-    const int r = e / (HD / 4), c = (e % (HD / 4)) * 4;
-    const T* p = val(r);
-    *reinterpret_cast<float4*>(&sm.kv[r][c]) = p ? load4<T>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  __syncthreads();
+  simt_wait1();
+  __syncthreads();  // P is complete, the values are there
   if (masked)
     simt_pv<HD, true>(sm, st);
   else
     simt_pv<HD, false>(sm, st);
+  __syncthreads();  // the values are consumed
+  next_v();
+  simt_commit();
 }
 
 // ---- host helpers --------------------------------------------------------------

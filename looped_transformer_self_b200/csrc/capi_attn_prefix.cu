@@ -8,11 +8,12 @@
 namespace lt {
 
 // fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs a) {
   extern __shared__ __align__(16) char smem_raw[];
   SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
-  __shared__ int slot[PREFIX_N];
+  // The slots of two blocks' keys stand in the key rows' padding: two CTAs fill an SM's shared memory.
+  auto slot_at = [&](int b, int j) -> int& { return reinterpret_cast<int&>(sm.k[j][HD + (b & 1)]); };
   const int tok = SIMT_M / a.group, group = a.group;
   pdl_trigger();
   pdl_wait();
@@ -29,9 +30,43 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
     walk.publish(a, threadIdx.x, SIMT_THREADS);
     const int b0 = walk.b0, b1 = b0 + walk.n;
     const int rows = pos.nrow * group, h0 = pos.kh * group;
-    const T* q = (const T*)a.q + (size_t)pos.row0 * a.sq + (size_t)h0 * HD;
-    __syncthreads();  // the previous tile's queries are consumed
-    simt_load_q<T, HD>(sm, [&](int r) -> const T* {
+    const float* q = (const float*)a.q + (size_t)pos.row0 * a.sq + (size_t)h0 * HD;
+    const int np = pos.g.np, nk = np + pos.tail.y - pos.tail.x;
+    const float* kc = (const float*)a.cache + (size_t)pos.kh * HD;
+    auto slot_of = [&](int b) {  // of this thread's key of block b
+      const int x = b * PREFIX_N + threadIdx.x;
+      int s = -1;
+      if (threadIdx.x < PREFIX_N && b < b1) {
+        if (x < np) s = __ldg(a.prefix + pos.g.p0 + x);
+        else if (x < nk) s = __ldg(a.tail + pos.tail.x + x - np);
+      }
+      return s >= 0 && s < a.n_slots ? s : -1;
+    };
+    auto put = [&](int b, int s) {
+      if (threadIdx.x < PREFIX_N) slot_at(b, threadIdx.x) = s;
+    };
+    auto fetch_k = [&](int b) {
+      if (b < b1)
+        simt_fetch<HD, HD + 4>(&sm.k[0][0], [&](int j) {
+          const int s = slot_at(b, j);
+          return s >= 0 ? kc + (size_t)s * 2 * width : nullptr;
+        }, q);
+    };
+    auto fetch_v = [&](int b) {
+      if (b < b1)
+        simt_fetch<HD, HD>(&sm.v[0][0], [&](int j) {
+          const int s = slot_at(b, j);
+          return s >= 0 ? kc + ((size_t)s * 2 + 1) * width : nullptr;
+        }, q);
+    };
+    __syncthreads();  // the previous tile is done with the shared arrays
+    put(b0, slot_of(b0));
+    __syncthreads();
+    fetch_k(b0);
+    simt_commit();
+    fetch_v(b0);
+    simt_commit();
+    simt_load_q<HD>(sm, [&](int r) {
       return r < rows ? q + (size_t)(r / group) * a.sq + (r % group) * HD : nullptr;
     }, a.scale);
     int2 mine[4];  // tail entries of this thread's rows, as key indices of the tile
@@ -41,32 +76,20 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
       mine[i] = {0, 0};
       if (r < rows) {
         const int2 t = off_range(a.tail_off, pos.row0 + r / group, a.n_tail, a.status);
-        mine[i] = {pos.g.np + t.x - pos.tail.x, pos.g.np + t.y - pos.tail.x};
+        mine[i] = {np + t.x - pos.tail.x, np + t.y - pos.tail.x};
       }
     }
-    const int np = pos.g.np, nk = np + pos.tail.y - pos.tail.x;
-    const T* kc = (const T*)a.cache + (size_t)pos.kh * HD;
     SimtState<HD> st;
     st.clear();
     for (int b = b0; b < b1; ++b) {
-      const int x0 = b * PREFIX_N;
-      __syncthreads();
-      if (threadIdx.x < PREFIX_N) {
-        const int x = x0 + threadIdx.x;
-        int s = -1;
-        if (x < np) s = __ldg(a.prefix + pos.g.p0 + x);
-        else if (x < nk) s = __ldg(a.tail + pos.tail.x + x - np);
-        slot[threadIdx.x] = s >= 0 && s < a.n_slots ? s : -1;
-      }
-      __syncthreads();
-      simt_block<T, HD>(
-          sm, st, [&](int j) -> const T* { return slot[j] >= 0 ? kc + (size_t)slot[j] * 2 * width : nullptr; },
-          [&](int j) -> const T* { return slot[j] >= 0 ? kc + ((size_t)slot[j] * 2 + 1) * width : nullptr; },
+      const int x0 = b * PREFIX_N, next = slot_of(b + 1);
+      simt_block<HD>(
+          sm, st,
           [&](int r, int j) {
             const int2 m = mine[r & 3];
-            return slot[j] >= 0 && (x0 + j < np || (x0 + j >= m.x && x0 + j < m.y));
+            return slot_at(b, j) >= 0 && (x0 + j < np || (x0 + j >= m.x && x0 + j < m.y));
           },
-          x0 + PREFIX_N > np);
+          x0 + PREFIX_N > np, [&] { put(b + 1, next); }, [&] { fetch_k(b + 1); }, [&] { fetch_v(b + 1); });
     }
     const size_t part = (size_t)(blockIdx.x + pos.t);
 #pragma unroll
@@ -150,8 +173,8 @@ static cudaError_t prefix_merge(const PrefixArgs& a, int grid, cudaStream_t st) 
 
 template <int HD>
 static cudaError_t prefix_f32(const PrefixArgs& a, int grid, cudaStream_t st) {
-  if (cudaError_t e = allow_smem<k_attn_prefix_simt<float, HD>>(sizeof(SimtSmem<HD>))) return e;
-  if (cudaError_t e = launch_pdl(k_attn_prefix_simt<float, HD>, grid, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a))
+  if (cudaError_t e = allow_smem<k_attn_prefix_simt<HD>>(sizeof(SimtSmem<HD>))) return e;
+  if (cudaError_t e = launch_pdl(k_attn_prefix_simt<HD>, grid, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a))
     return e;
   return prefix_merge<float, HD, SIMT_M>(a, grid, st);
 }

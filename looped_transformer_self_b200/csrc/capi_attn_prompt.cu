@@ -8,7 +8,7 @@
 namespace lt {
 
 // fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prompt_simt(PromptArgs a) {
   extern __shared__ __align__(16) char smem_raw[];
   SimtSmem<HD>& sm = *reinterpret_cast<SimtSmem<HD>*>(smem_raw);
@@ -20,21 +20,33 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prompt_simt(PromptArgs
   const int t0 = pt.tile * tok, nt = min(tok, pt.lq - t0), rows = nt * a.group;
   const int ctx = pt.lk - pt.lq;  // keys before the first query
   const int group = a.group, h0 = kh * group;
-  const T* q = (const T*)a.q + (size_t)(pt.q0 + t0) * a.sq + (size_t)h0 * HD;
-  const T* k = (const T*)a.k + (size_t)pt.k0 * a.sk + (size_t)kh * HD;
-  const T* v = (const T*)a.v + (size_t)pt.k0 * a.sv + (size_t)kh * HD;
-  simt_load_q<T, HD>(sm, [&](int r) -> const T* {
+  const float* q = (const float*)a.q + (size_t)(pt.q0 + t0) * a.sq + (size_t)h0 * HD;
+  const float* k = (const float*)a.k + (size_t)pt.k0 * a.sk + (size_t)kh * HD;
+  const float* v = (const float*)a.v + (size_t)pt.k0 * a.sv + (size_t)kh * HD;
+  const int see_first = ctx + t0 + 1, see_last = min(ctx + t0 + nt, pt.lk);  // keys of the first / last row
+  auto fetch_k = [&](int b) {
+    if (b < see_last)
+      simt_fetch<HD, HD + 4>(&sm.k[0][0],
+                             [&](int j) { return b + j < see_last ? k + (size_t)(b + j) * a.sk : nullptr; }, q);
+  };
+  auto fetch_v = [&](int b) {
+    if (b < see_last)
+      simt_fetch<HD, HD>(&sm.v[0][0],
+                         [&](int j) { return b + j < see_last ? v + (size_t)(b + j) * a.sv : nullptr; }, q);
+  };
+  fetch_k(0);
+  simt_commit();
+  fetch_v(0);
+  simt_commit();
+  simt_load_q<HD>(sm, [&](int r) {
     return r < rows ? q + (size_t)(r / group) * a.sq + (r % group) * HD : nullptr;
   }, a.scale);
   SimtState<HD> st;
   st.clear();
-  const int see_first = ctx + t0 + 1, see_last = min(ctx + t0 + nt, pt.lk);  // keys of the first / last row
   for (int b = 0; b < see_last; b += SIMT_N) {
-    simt_block<T, HD>(
-        sm, st, [&](int j) -> const T* { return b + j < see_last ? k + (size_t)(b + j) * a.sk : nullptr; },
-        [&](int j) -> const T* { return b + j < see_last ? v + (size_t)(b + j) * a.sv : nullptr; },
-        [&](int r, int j) { return b + j <= ctx + t0 + r / group && b + j < see_last; },
-        b + SIMT_N > see_first);
+    simt_block<HD>(
+        sm, st, [&](int r, int j) { return b + j <= ctx + t0 + r / group && b + j < see_last; },
+        b + SIMT_N > see_first, [] {}, [&] { fetch_k(b + SIMT_N); }, [&] { fetch_v(b + SIMT_N); });
   }
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
@@ -42,21 +54,19 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prompt_simt(PromptArgs
     const int r = ty * 4 + i;
     if (r >= rows) continue;
     const float inv = st.l[i] > 0.f ? 1.f / st.l[i] : st.l[i] == 0.f ? 0.f : st.l[i];
-    T* o = (T*)a.o + (size_t)(pt.q0 + t0 + r / group) * a.so + (size_t)(h0 + r % group) * HD;
+    float* o = (float*)a.o + (size_t)(pt.q0 + t0 + r / group) * a.so + (size_t)(h0 + r % group) * HD;
 #pragma unroll
-    for (int c = 0; c < HD / 32; ++c) {
-      o[tx * 2 + 32 * c] = from_f<T>(st.o[i][2 * c] * inv);
-      o[tx * 2 + 32 * c + 1] = from_f<T>(st.o[i][2 * c + 1] * inv);
-    }
+    for (int c = 0; c < HD / 32; ++c)
+      *reinterpret_cast<float2*>(o + tx * 2 + 32 * c) = make_float2(st.o[i][2 * c] * inv, st.o[i][2 * c + 1] * inv);
   }
 }
 
-template <typename T, int HD>
+template <int HD>
 static cudaError_t prompt_simt(const PromptArgs& a, cudaStream_t st) {
   const int tok = SIMT_M / a.group;
   const unsigned tiles = (unsigned)(a.n_q / tok + a.n_seqs);
-  if (cudaError_t e = allow_smem<k_attn_prompt_simt<T, HD>>(sizeof(SimtSmem<HD>))) return e;
-  return launch_pdl(k_attn_prompt_simt<T, HD>, tiles * a.kv_heads, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a);
+  if (cudaError_t e = allow_smem<k_attn_prompt_simt<HD>>(sizeof(SimtSmem<HD>))) return e;
+  return launch_pdl(k_attn_prompt_simt<HD>, tiles * a.kv_heads, 1, SIMT_THREADS, sizeof(SimtSmem<HD>), st, a);
 }
 
 template <int HD>
@@ -85,7 +95,7 @@ static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
 template <int HD>
 static int prompt_any(int dtype, const PromptArgs& a, cudaStream_t st) {
   if (dtype == LT_BF16) return prompt_tc<HD>(a, st);
-  return prompt_simt<float, HD>(a, st) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
+  return prompt_simt<HD>(a, st) == cudaSuccess ? LT_OK : LT_ERR_CUDA;
 }
 
 }  // namespace lt
