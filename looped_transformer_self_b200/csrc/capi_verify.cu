@@ -140,7 +140,6 @@ __global__ void __launch_bounds__(VERIFY_THREADS, 4) k_verify(VerifyArgs a, int 
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int s = blockIdx.x / nr, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  pdl_trigger();
   pdl_wait();
   const int o0 = __ldg(a.off + s), o1 = __ldg(a.off + s + 1);
   const bool bad = o0 < 0 || o1 < o0 || o1 > a.n_drafts;  // the same in every CTA of the cluster
@@ -292,11 +291,12 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
   if (!d_p || !d_off || !d_u_draw || !d_n_accepted || !d_tokens || stride_p < V ||
       (n_drafts > 0 && (!d_draft || !d_u_accept)) || (d_q && stride_q < V))
     return LT_ERR_ARG;
-  // Eight CTAs a sequence for latency (one chain at a vocabulary of 49152: 7.1 us, 18.2 us with one),
-  // fewer where all of them would not be resident at once (192 chains at 65536: 26.7 us with two,
+  // Eight CTAs a sequence for latency (one chain at a vocabulary of 49152: 6.9 us, 18.2 us with one),
+  // fewer where all of them would not be resident at once with room to place the clusters (148 chains
+  // at 65536: 23.0 us with two, 25.7 us with four, which would just fit; 192 chains: 26.2 us with two,
   // 33.2 us with eight) or would have less than a segment per warp.
   int nr = 8;
-  while (nr > 1 && ((long long)n_seqs * nr > 4ll * attn_sm_count() || (long long)(nr / 2) * VERIFY_WARPS * VERIFY_SEG >= V)) nr /= 2;
+  while (nr > 1 && ((long long)n_seqs * nr > 3ll * attn_sm_count() || (long long)(nr / 2) * VERIFY_WARPS * VERIFY_SEG >= V)) nr /= 2;
   const long long segs = ((long long)V + VERIFY_SEG - 1) / VERIFY_SEG;
   const int units = (int)((segs + (long long)nr * VERIFY_MAX_SEGS - 1) / ((long long)nr * VERIFY_MAX_SEGS));
   VerifyArgs a = {d_p, d_q, stride_p, stride_q, d_draft, d_off, n_seqs, n_drafts, V, d_u_accept,
