@@ -117,8 +117,9 @@ __device__ __forceinline__ bool drop_nonfinite(uint32_t& x) {
 // chunk of the head).  A box of (64, heads, tokens, chunks) lands as one
 // 128-byte-swizzled tile of heads x tokens rows per chunk.  Head size 96 keeps
 // its 96 elements in the first dimension (the box's second half reads zeros
-// past them), so that no box reads past a head.
+// past them), so that no box reads past a head.  A box of several chunks packs
+// them by its rows: only boxes of 128 rows take both chunks of a head at once.
 int attn_tmap(CUtensorMap* map, const void* base, int hd, int heads, long long tokens, long long stride,
-              int box_heads, int box_tokens);
+              int box_heads, int box_tokens, int box_chunks);
 
 }  // namespace lt

@@ -191,7 +191,7 @@ template <int HD>
 static cudaError_t prefix_tc(const PrefixArgs& a, int grid, cudaStream_t st) {
   using W = PrefixWork;
   CUtensorMap mq;
-  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_rows, a.sq, a.group, 128 / a.group)) return cudaErrorInvalidValue;
+  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_rows, a.sq, a.group, 128 / a.group, 1)) return cudaErrorInvalidValue;
   if (cudaError_t e = allow_smem<k_attn_tc<HD, W>>(tc_smem<HD, W>())) return e;
   if (cudaError_t e = launch_pdl(k_attn_tc<HD, W>, grid, 1, W::THREADS, tc_smem<HD, W>(), st, a, mq, mq, mq)) return e;
   return prefix_merge<__nv_bfloat16, HD, 256>(a, grid, st);

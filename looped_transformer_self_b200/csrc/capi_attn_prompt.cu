@@ -78,8 +78,8 @@ static int prompt_tc(const PromptArgs& a, cudaStream_t st) {
   const void* k = a.n_kv > 0 ? a.k : a.q;
   const void* v = a.n_kv > 0 ? a.v : a.q;
   const long long nk = a.n_kv > 0 ? a.n_kv : 1;
-  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_q, a.sq, a.group, tok) ||
-      attn_tmap(&mk, k, HD, a.kv_heads, nk, a.sk, 1, 128) || attn_tmap(&mv, v, HD, a.kv_heads, nk, a.sv, 1, 128))
+  if (attn_tmap(&mq, a.q, HD, a.heads, a.n_q, a.sq, a.group, tok, 1) ||
+      attn_tmap(&mk, k, HD, a.kv_heads, nk, a.sk, 1, 128, 2) || attn_tmap(&mv, v, HD, a.kv_heads, nk, a.sv, 1, 128, 2))
     return LT_ERR_CUDA;
   if (allow_smem<k_attn_tc<HD, W>>(tc_smem<HD, W>()) != cudaSuccess) return LT_ERR_CUDA;
   const unsigned pairs = (unsigned)prompt_pairs(a.n_q, a.n_seqs, a.group) * a.kv_heads;

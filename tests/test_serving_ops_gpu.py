@@ -68,6 +68,18 @@ def test_prompt_matches_64_bits(dtype, H, Hk, hd, lq, ctx):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("group", [3, 5, 7, 11, 33, 48])
+@pytest.mark.parametrize("hd", [32, 64, 96, 128])
+def test_prompt_groups_that_do_not_fill_a_tile(group, hd):
+    """Query heads per key/value head that do not divide 128: tiles of fewer rows."""
+    from looped_transformer_self_b200.binding import attn_prompt
+    lq, lk = [77, 1, 190], [77, 90, 400]
+    q, k, v = _prompt_inputs("bf16", 2 * group, 2, hd, lq, lk)
+    got = attn_prompt(q, k, v, _off(lq), _off(lk))
+    want, tol = R.prompt(q, k, v, lq, lk, hd ** -0.5)
+    _close(got, want, tol)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prompt_fused_rows_padding_and_output_stride(dtype):
     """q, k, v as parts of one projection; rows behind the last sequence (NaN on
@@ -249,6 +261,72 @@ def test_prefix_unseen_values_do_not_reach_a_row(dtype, H, Hk, hd, bad):
     assert bool((hit.isnan() if bad != bad else hit == bad).all())
     other = [c for c in range(hd) if c != 7]
     _close(got[4][:, other], want[4][:, other], tol[4][:, other])
+
+
+# Sizes at which bf16 takes the tensor-core tiles (many keys): one short tile, tiles in both halves,
+# ragged groups, several tiles per group, every head size, parts of odd lengths.
+LONG_PREFIXES = [
+    (16, 16, 128, [8], [10500], 4),
+    (32, 8, 128, [32], [3100], 20),
+    (32, 8, 128, [70, 1], [2500, 3000], 9),
+    (8, 2, 64, [40, 0, 3, 9], [9000, 500, 700, 5000], 40),
+    (55, 55, 96, [5, 2], [1500, 1601], 6),
+    (14, 2, 96, [19], [13001], 64),
+    (64, 1, 32, [3, 5], [24000, 300], 2),
+    (6, 2, 128, [50], [12100], 0),
+    (16, 16, 32, [1], [10127], 1),
+    (16, 4, 128, [4] * 30, [260] * 30, 3),
+]
+
+
+@pytest.mark.parametrize("H,Hk,hd,rows,np_,most", LONG_PREFIXES)
+def test_prefix_with_many_keys_matches_64_bits(H, Hk, hd, rows, np_, most):
+    r = random.Random(sum(rows) + most)
+    nt = [r.randint(0, most) for _ in range(sum(rows))]
+    q, cache, prefixes, tails = _prefix_inputs("bf16", H, Hk, hd, rows, np_, nt)
+    for p in prefixes:  # padding inside the lists
+        for i in range(7, len(p), 991):
+            p[i] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    got = _prefix_call(q, cache, rows, prefixes, tails, status=status, out=out)
+    some = sorted(r.sample(range(sum(rows)), min(12, sum(rows))))
+    first = [sum(rows[:g]) for g in range(len(rows))]
+    for i in some:  # 64-bit rows one by one
+        g = max(k for k in range(len(rows)) if first[k] <= i and rows[k])
+        want, tol = R.prefix(q[i:i + 1], cache, [1], [prefixes[g]], [tails[i]], hd ** -0.5)
+        _close(got[i:i + 1], want, tol)
+    assert int(status) == 0
+    again = _prefix_call(q, cache, rows, prefixes, tails)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,Hk,hd,n", [(16, 16, 128, 10500), (32, 4, 96, 7000)])
+def test_prefix_with_many_keys_keeps_unseen_values_out(H, Hk, hd, n, bad):
+    """A bad value in one row's tail reaches that row alone, one in the prefix every row; bad
+    slots that no list names reach nobody; a row without keys gets zeros."""
+    rows = [9, 2]
+    q, cache, prefixes, tails = _prefix_inputs("bf16", H, Hk, hd, rows, [n, 0], [3] * 11)
+    tails[10] = [-1, -1]
+    want, tol = R.prefix(q, cache, rows, prefixes, tails, hd ** -0.5)
+    named = {s for l in prefixes + tails for s in l}
+    rest = torch.tensor([s for s in range(cache.shape[0]) if s not in named], device="cuda")
+    cache[rest] = bad
+    kv = cache.view(-1, 2, Hk, hd)
+    kv[tails[4][1], 1, :, 7] = bad
+    got = _prefix_call(q, cache, rows, prefixes, tails)
+    other = [c for c in range(hd) if c != 7]
+    clean = [i for i in range(11) if i != 4]
+    _close(got[clean], want[clean], tol[clean])
+    _close(got[4][:, other], want[4][:, other], tol[4][:, other])
+    hit = got[4, :, 7].double()
+    assert bool((hit.isnan() if bad != bad else hit == bad).all()) and bool((got[10] == 0).all())
+    kv[prefixes[0][n - 1], 1, :, 9] = bad  # the last key of the prefix: a block that holds tails too
+    got = _prefix_call(q, cache, rows, prefixes, tails)
+    hit = got[:9, :, 9].double()
+    assert bool((hit.isnan() if bad != bad else hit == bad).all())
+    _close(got[9:], want[9:], tol[9:])
 
 
 def test_prefix_slots_past_two_gigabytes():
