@@ -20,10 +20,14 @@
 // overflows and the relative rounding of a weight is the same at any scale.
 //
 // What bounds it: a tile's chain of load S, maximum, 128 exponentials a thread,
-// product and next S, about 3500 cycles per block of both tiles at head size 128
-// against 2048 of the tensor pipe; the exponentials are 1500 of them.  Two
-// threads per row (16 softmax warps), exponentials on the FMA pipe (polynomial
-// of degree 5) and P in halves were measured and were not faster.
+// product and next S, about 3400 cycles per block of both tiles at head size 128
+// against 2048 of the tensor pipe (1536 at 96); the exponentials are 1500 of
+// them.  Measured and not faster: two threads per row (16 softmax warps);
+// exponentials on the FMA pipe (polynomial of degree 5); P in halves; half
+// blocks of 64 keys with two S buffers a tile, so that a tile's next S runs
+// under its softmax (11 % faster at head size 96, 5 to 11 % slower at 128 and
+// for the slot cache: products of 64 columns take 3/4 of the tensor rate);
+// outputs turned in shared memory before they are stored.
 #pragma once
 
 #include "attn_tc.cuh"
@@ -114,21 +118,21 @@ __device__ __forceinline__ int clc_answer(uint32_t at) {
   return ok ? (int)x : -1;
 }
 
-// What an item covers: per tile first token, tokens and half blocks, and the
-// ring's blocks jb .. jb + n - 1.  The tiles share every block (step 1), except that
+// What an item covers: per tile first token, tokens and blocks, and the ring's
+// blocks jb .. jb + n - 1.  The tiles share every block (step 1), except that
 // where the second tile is empty its rows may be the first's (step 2): then the
 // tiles take the blocks in turn and leave a partial each.
 struct TcSpan {
-  int t0[2], nt[2], nh[2], n, jb, step;  // nh: a tile's half blocks of 64 keys
+  int t0[2], nt[2], nb[2], n, jb, step;
   __device__ __forceinline__ void share_rows() {
     step = 2;
     t0[1] = t0[0];
     nt[1] = nt[0];
-    nh[0] = (n + 1) / 2 * 2;
-    nh[1] = n / 2 * 2;
+    nb[1] = n >> 1;
+    nb[0] = n - nb[1];
   }
-  // ring block of the tile's h-th half, from jb
-  __device__ __forceinline__ int at(int t, int h) const { return step == 2 ? (h & ~1) + t : h >> 1; }
+  // ring block of the tile's k-th block, from jb
+  __device__ __forceinline__ int at(int t, int k) const { return step == 2 ? 2 * k + t : k; }
 };
 
 // lt_attn_prompt: a pair of tiles of one sequence, or one of `splits` ranges of
@@ -157,12 +161,9 @@ struct PromptWork {
     }
     const int chunk = cdiv(max(full[0], full[1]), splits);
     s.jb = it.split * chunk;
-    s.n = max(0, min(max(full[0], full[1]) - s.jb, chunk));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {  // keys of the range that the tile's last row sees
-      const int keys = min(it.lk - it.lq + s.t0[i] + s.nt[i], (s.jb + s.n) * 128) - s.jb * 128;
-      s.nh[i] = s.nt[i] ? cdiv(max(0, keys), 64) : 0;
-    }
+    for (int i = 0; i < 2; ++i) s.nb[i] = max(0, min(full[i] - s.jb, chunk));
+    s.n = max(s.nb[0], s.nb[1]);
     s.step = 1;
     if (splits > 1 && s.nt[1] == 0) s.share_rows();
     return s;
@@ -191,7 +192,7 @@ struct PrefixWork {
     for (int i = 0; i < 2; ++i) {
       s.t0[i] = i * tok;
       s.nt[i] = max(0, min(tok, it.lq - s.t0[i]));
-      s.nh[i] = s.nt[i] ? max(1, min(cdiv(it.nk - it.jb * 128, 64), 2 * it.n)) : 0;
+      s.nb[i] = s.nt[i] ? it.n : 0;
     }
     s.n = it.n;
     s.jb = it.jb;
@@ -207,7 +208,7 @@ struct TcSmem {
   alignas(16) uint4 clc;  // answer of a cancel request
   uint64_t clc_full, loaded;
   uint64_t item_full[TC_ITEMS], item_empty[TC_ITEMS];
-  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2][2], p_full[2][2], o_done[2][2], fin;
+  uint64_t q_full, q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2][4], o_done[2], turn[2], fin;
   uint32_t tmem;
   int abort_flag;
   int poison[4];  // by item: (its number + 1) once a masked block held an infinity or NaN among its values
@@ -252,11 +253,9 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   const uint32_t q_full = smem_u32(&sb.q_full), q_empty = smem_u32(&sb.q_empty), fin = smem_u32(&sb.fin);
   auto kv_full = [&](int s) { return smem_u32(&sb.kv_full[s]); };
   auto kv_empty = [&](int s) { return smem_u32(&sb.kv_empty[s]); };
-  // The n-th half block of a tile has buffer n & 1 of S (and P) and phase n / 2 of its barriers: S of
-  // n is only issued behind the product of n - 2, so a phase waited for is at most one away.
-  auto s_full = [&](int t, int n) { return smem_u32(&sb.s_full[t][n & 1]); };
-  auto p_full = [&](int t, int n) { return smem_u32(&sb.p_full[t][n & 1]); };
-  auto o_done = [&](int t, int n) { return smem_u32(&sb.o_done[t][n & 1]); };
+  auto s_full = [&](int t) { return smem_u32(&sb.s_full[t]); };
+  auto p_full = [&](int t, int c) { return smem_u32(&sb.p_full[t][c]); };
+  auto o_done = [&](int t) { return smem_u32(&sb.o_done[t]); };
   volatile int* abort_flag = &sb.abort_flag;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -273,11 +272,10 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       mbar_init(kv_empty(s), 2);  // both tiles
     }
     for (int t = 0; t < 2; ++t) {
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(s_full(t, i), 1);
-        mbar_init(p_full(t, i), 4);  // four warps
-        mbar_init(o_done(t, i), 1);
-      }
+      mbar_init(s_full(t), 1);
+      for (int c = 0; c < 4; ++c) mbar_init(p_full(t, c), 4);  // four warps
+      mbar_init(o_done(t), 1);
+      mbar_init(smem_u32(&sb.turn[t]), 4);  // four warps of the other tile
     }
     if (GATHER)
       for (int i = 0; i < TC_VALID; ++i) mbar_init(smem_u32(&sb.valid_full[i]), 4);
@@ -296,7 +294,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   tc_fence_after();
   pdl_wait();
   const uint32_t tmem = sb.tmem;
-  auto s_col = [&](int t, int n) { return tmem + (uint32_t)(t * 128 + (n & 1) * 64); };
+  auto s_col = [&](int t) { return tmem + (uint32_t)t * 128; };
   auto o_col = [&](int t) { return tmem + 256 + (uint32_t)t * C::OCOLS; };
   // use u of the ring: K and V of the items' blocks in turn
   auto slot_of = [&](int u) { return u % C::SLOTS; };
@@ -437,30 +435,22 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       // warp walks through the items and waits; one elected lane issues (a loop run by one lane alone
       // cost up to 250 cycles per MMA here: its operands do not stay in uniform registers).  MMAs of
       // one thread run in order, so S may be written over the P of the product before it.
-      constexpr uint32_t IS = attn_idesc(64, false), IO = attn_idesc(HD, true);
+      constexpr uint32_t IS = attn_idesc(128, false), IO = attn_idesc(HD, true);
       const int t = warp - 9;
       // descriptors count 16-byte units: a step along an operand is an addition
       const uint64_t dq = smem_desc(q_s + t * C::TILE), dk = smem_desc(ring), dv = smem_desc_mn(ring, 16384);
-      const uint32_t ot = o_col(t);
+      const uint32_t st = s_col(t), ot = o_col(t), s_bar = s_full(t), o_bar = o_done(t);
       auto wait = [&](uint32_t bar, uint32_t par) {
         return __all_sync(0xffffffffu, mbar_try_wait(bar, par)) ||
                __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag));
       };
-      auto full = [&](int u) {
-        const bool r = wait(kv_full(slot_of(u)), par_of(u));
-        if (GATHER) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        return r;
-      };
-      int ub = 0, given = 0, done = 0, qn = 0;  // ring uses of items before, given back; half blocks before
-      // Gives back the ring's uses below u.  Both tiles give back each use, needed or not, and not
-      // before it is full: no tile gets a turn of the ring ahead.
-      auto give = [&](int u) {
-        for (; given < u; ++given) {
-          if (!wait(kv_full(slot_of(given)), par_of(given))) return false;
-          if (elect_one()) tc_commit(kv_empty(slot_of(given)));
-          __syncwarp();
+      int slot = 0, done = 0, qn = 0;
+      uint32_t ring_par = 0;
+      auto next_slot = [&] {
+        if (++slot == C::SLOTS) {
+          slot = 0;
+          ring_par ^= 1;
         }
-        return true;
       };
       bool ok = true;
       Item item;
@@ -471,49 +461,68 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         __syncwarp();
         if (lane == 0) give_back(it);
         if (sp.n == 0) continue;
-        const int nh = t ? sp.nh[1] : sp.nh[0];
+        const int nb = t ? sp.nb[1] : sp.nb[0];
         if (!(ok = wait(q_full, (uint32_t)qn & 1))) break;
         ++qn;
-        // Step h: the product of half block h - 2's weights, then S of half block h over them.
-        for (int h = 0; h < nh + 2 || h == 0; ++h) {
-          if (h >= 2 && h - 2 < nh) {
-            const int g = h - 2, n = done + g, u = ub + 2 * sp.at(t, g) + 1;
-            if (!(ok = full(u) && wait(p_full(t, n), (uint32_t)(n >> 1) & 1))) break;
-            tc_fence_after();
-            const uint64_t v = dv + (uint32_t)(slot_of(u) * (C::TILE >> 4) + (g & 1) * 512);
-            if (elect_one()) {
+        // Step j: the product of block j - 1's weights, then S of block j.  A slot is given back by
+        // both tiles, used or not, and not before it is full: no tile gets a turn of the ring ahead.
+        int v_slot = 0, s_next = 0, p_next = 0;  // blocks whose S is out; the one whose product follows, + 1
+        uint32_t v_par = 0;
+        for (int j = 0; j <= sp.n; ++j) {
+          const int k_slot = slot;
+          const uint32_t k_par = ring_par;
+          if (j > 0 && !(ok = wait(kv_full(v_slot), v_par))) break;
+          if (GATHER) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (p_next > 0) {
+            const uint64_t v = dv + (uint32_t)(v_slot * (C::TILE >> 4));
+            const uint32_t par = (uint32_t)(done + p_next - 1) & 1;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                tc_mma_ts(ot, s_col(t, n) + i * 8, v + i * 128, IO, g > 0 || i > 0);
-              tc_commit(o_done(t, n));
-            }
-            __syncwarp();
-          }
-          if (h < nh) {
-            const int n = done + h, u = ub + 2 * sp.at(t, h);
-            if (!(ok = full(u))) break;
-            tc_fence_after();
-            const uint64_t k = dk + (uint32_t)(slot_of(u) * (C::TILE >> 4) + (h & 1) * 512);
-            if (elect_one()) {
+            for (int c = 0; c < 4; ++c) {
+              if (!(ok = ok && wait(p_full(t, c), par))) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-              for (int i = 0; i < HD / 16; ++i) {
-                const uint32_t at = ((uint32_t)(i >> 2) * 16384 + (i & 3) * 32) >> 4;
-                tc_mma<false>(s_col(t, n), dq + at, k + at, IS, i > 0);
+                for (int i = 2 * c; i < 2 * c + 2; ++i)
+                  tc_mma_ts(ot, st + i * 8, v + i * 128, IO, p_next > 1 || i > 0);
+                if (c == 3) tc_commit(o_bar);
               }
-              tc_commit(s_full(t, n));
-              if (h + 1 == nh) tc_commit(q_empty);
+              __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
+            p_next = 0;
           }
-          // needed next: the values of half block h - 1
-          if (h >= 1 && h - 1 < nh && !(ok = give(ub + 2 * sp.at(t, h - 1) + 1))) break;
+          if (j < sp.n) {
+            if (!(ok = wait(kv_full(k_slot), k_par))) break;
+            if (GATHER) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (s_next < nb && j == sp.at(t, s_next)) {
+              p_next = ++s_next;
+              tc_fence_after();
+              const uint64_t k = dk + (uint32_t)(k_slot * (C::TILE >> 4));
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < HD / 16; ++i) {
+                  const uint32_t at = ((uint32_t)(i >> 2) * 16384 + (i & 3) * 32) >> 4;
+                  tc_mma<false>(st, dq + at, k + at, IS, i > 0);
+                }
+                tc_commit(s_bar);
+              }
+              __syncwarp();
+            }
+            next_slot();
+          }
+          if (elect_one()) {
+            if (j > 0) tc_commit(kv_empty(v_slot));
+            if (j < sp.n) tc_commit(kv_empty(k_slot));
+            if (j + 1 == sp.n) tc_commit(q_empty);
+          }
+          __syncwarp();
+          if (j < sp.n) {
+            v_slot = slot;
+            v_par = ring_par;
+            next_slot();
+          }
         }
-        if (!ok) break;
-        if (nh == 0 && elect_one()) tc_commit(q_empty);
-        __syncwarp();
-        ub += 2 * sp.n;
-        if (!(ok = give(ub))) break;
-        done += nh;
+        done += nb;
       }
       if (*abort_flag) {  // MMAs in flight end before TMEM is freed
         int none = 0;
@@ -590,7 +599,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = threadIdx.x & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t oc = o_col(t) + lane_off;
+    const uint32_t sc = s_col(t) + lane_off, oc = o_col(t) + lane_off;
     const int tl = r / group;                        // token within the tile
     const float sl = a.scale * 1.4426950408889634f;  // scores in log2 units
     const float slack = fminf(8.f / sl, 1e30f);
@@ -600,13 +609,23 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       return __all_sync(0xffffffffu, mbar_try_wait(bar, par)) ||
              __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag));
     };
+    // The tiles take turns with their exponentials, one turn per block of the item (a tile without the
+    // block passes): left alone they fall into step, both in their softmax and then both waiting for
+    // the tensor core.
+    int turns = 0;
+    const uint32_t my_turn = smem_u32(&sb.turn[t]), other_turn = smem_u32(&sb.turn[t ^ 1]);
+    auto take_turn = [&](int k) { return wait(my_turn, (uint32_t)(turns + k + (t ^ 1)) & 1); };
+    auto pass_turn = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(other_turn);
+    };
     for (int it = 0; ok; ++it) {
       Item item;
       ok = __all_sync(0xffffffffu, take(it, item));
       if (!ok) break;
       if (lane == 0) give_back(it);
       const TcSpan sp = W::span(item, tok, a);
-      const int t0 = t ? sp.t0[1] : sp.t0[0], nt = t ? sp.nt[1] : sp.nt[0], nh = t ? sp.nh[1] : sp.nh[0];
+      const int t0 = t ? sp.t0[1] : sp.t0[0], nt = t ? sp.nt[1] : sp.nt[0], nb = t ? sp.nb[1] : sp.nb[0];
       const bool valid = tl < nt && r < tok * group;
       // Keys a row sees: [0, see) and, of the slot cache, also [own.x, own.y).  Keys from `shared` on
       // are not seen by all rows of the tile.
@@ -624,30 +643,28 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         shared = ctx + t0 + 1;
       }
       float m = -INFINITY, l = 0.f;                   // m: reference maximum of the raw scores
-      for (int h = 0; h < nh; ++h) {
-        const int jr = sp.at(t, h), n = done + h;
-        const int key0 = (sp.jb + jr) * 128 + (h & 1) * 64;  // first key of the half block
-        const uint32_t sc = s_col(t, n) + lane_off;
-        if (!(ok = wait(s_full(t, n), (uint32_t)(n >> 1) & 1))) break;
+      for (int jj = 0; jj < nb; ++jj) {
+        const int jr = sp.at(t, jj), j = sp.jb + jr, ph = done + jj;
+        if (!(ok = wait(s_full(t), ph & 1))) break;
         tc_fence_after();
-        uint32_t x[64];
-        tmem_ld32(sc, x);
-        tmem_ld32(sc + 32, x + 32);
+        uint32_t x[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, x + c * 32);
         tmem_wait_ld();
-        const bool mixed = key0 + 64 > shared;  // holds keys that some row does not see
+        const bool mixed = (j + 1) * 128 > shared;  // holds keys that some row does not see
         bool masked = mixed;
         const uint32_t* there = nullptr;
         if constexpr (GATHER) {
           // the loads are fewer than TC_VALID blocks ahead, so the marks stay
           const int b = (ub >> 1) + jr;
           if (!(ok = wait(smem_u32(&sb.valid_full[b & (TC_VALID - 1)]), (uint32_t)(b / TC_VALID) & 1))) break;
-          there = sb.valid[b & (TC_VALID - 1)] + (h & 1) * 2;
-          masked = mixed || (there[0] & there[1]) != 0xffffffffu;
+          there = sb.valid[b & (TC_VALID - 1)];
+          masked = mixed || (there[0] & there[1] & there[2] & there[3]) != 0xffffffffu;
         }
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int x0 = key0 + c * 32;
+          for (int c = 0; c < 4; ++c) {
+            const int x0 = j * 128 + c * 32;
             uint32_t seen = bit_range(0, see - x0);
             if constexpr (GATHER) seen = (seen | bit_range(own.x - x0, own.y - x0)) & there[c];
 #pragma unroll
@@ -658,18 +675,17 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         if (mixed) {
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
-          // that see them at the end.  Two threads go over one key's row.
+          // that see them at the end.  A thread goes over one key's row.
           const int u = ub + 2 * jr + 1;
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
-          const int kr = (h & 1) * 64 + (r & 63), k0 = (r >> 6) * (HD / 16);  // row, first 16-byte piece
-          char* row = smem_raw + (2 + slot_of(u)) * C::TILE + kr * 128;
+          char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
           bool gone = false;  // an absent slot's row is zero already
-          if constexpr (!GATHER) gone = key0 + (r & 63) >= item.lk;
+          if constexpr (!GATHER) gone = j * 128 + r >= item.lk;
           uint32_t bad = 0;
 #pragma unroll
-          for (int k = k0; k < k0 + HD / 16; ++k) {
+          for (int k = 0; k < HD / 8; ++k) {
             // a key's 16-byte pieces lie at places given by its row (the swizzle)
-            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (kr & 7)) << 4));
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4));
             bad |= nonfinite_bits(v.x) | nonfinite_bits(v.y) | nonfinite_bits(v.z) | nonfinite_bits(v.w);
           }
           if (gone || bad) {
@@ -678,8 +694,8 @@ __global__ void __launch_bounds__(W::THREADS, 1)
               __threadfence_block();  // a warp that finds the value gone finds the flag set
             }
 #pragma unroll 1
-            for (int k = k0; k < k0 + HD / 16; ++k) {
-              uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (kr & 7)) << 4));
+            for (int k = 0; k < HD / 8; ++k) {
+              uint4* q = reinterpret_cast<uint4*>(row + (k >> 3) * 16384 + (((k & 7) ^ (r & 7)) << 4));
               uint4 v = *q;
               if (gone) v = make_uint4(0u, 0u, 0u, 0u);
               drop_nonfinite(v.x);
@@ -695,22 +711,22 @@ __global__ void __launch_bounds__(W::THREADS, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx4[e] = __uint_as_float(x[e]);
 #pragma unroll
-        for (int c = 4; c < 60; c += 8)
+        for (int c = 4; c < 124; c += 8)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             mx4[e] = fmaxf(fmaxf(mx4[e], __uint_as_float(x[c + e])), __uint_as_float(x[c + 4 + e]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], __uint_as_float(x[60 + e]));
+        for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], __uint_as_float(x[124 + e]));
         // (a NaN score leaves the maximum and comes out in its weight and the sum)
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         const bool grow = mx > m + slack;
-        if (h == 0) {
+        if (jj == 0) {
           m = mx;
         } else if (__any_sync(0xffffffffu, grow)) {
           const float f = grow ? ex2((m - mx) * sl) : 1.f;
           if (grow) m = mx;
           l *= f;
-          if (!(ok = wait(o_done(t, n - 1), (uint32_t)((n - 1) >> 1) & 1))) break;
+          if (!(ok = wait(o_done(t), (ph - 1) & 1))) break;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < HD; c += 16) {
@@ -727,25 +743,36 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         if (!(fabsf(ms) < INFINITY)) ms = m == -INFINITY ? 0.f : NAN;
         const uint64_t sl2 = pack2(sl, sl), ms2 = pack2(-ms, -ms);
         uint64_t sum[2] = {0, 0};
-        softmax_chunk(x, sl2, ms2, sum);
-        tmem_st16(sc, x);
-        softmax_chunk(x + 32, sl2, ms2, sum);
-        tmem_st16(sc + 16, x + 32);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t, n));
+        if (!(ok = take_turn(jj))) break;
+        // a quarter's store is waited for after the next quarter's exponentials
+#pragma unroll
+        for (int c = 0; c <= 4; ++c) {
+          if (c < 4) softmax_chunk(x + c * 32, sl2, ms2, sum);
+          if (c == 3) pass_turn();
+          if (c > 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full(t, c - 1));
+          }
+          if (c < 4) tmem_st16(sc + c * 16, x + c * 32);
+        }
         float s0, s1;
         unpack2(add2(sum[0], sum[1]), s0, s1);
         l += s0 + s1;
       }
+      const int most = max(sp.nb[0], sp.nb[1]);
+      for (int k = nb; ok && k < most; ++k) {
+        ok = take_turn(k);
+        pass_turn();
+      }
+      turns += most;
       if (!ok) break;
       const bool partial = W::partial(a);
-      if (GATHER && nh == 0 && valid) a.part_ml[(size_t)item.part * 256 + t * 128 + r] = make_float2(-INFINITY, 0.f);
-      if (nt > 0 && (nh > 0 || !partial)) {
-        if (nh > 0) {
-          const int n = done + nh - 1;
-          if (!(ok = wait(o_done(t, n), (uint32_t)(n >> 1) & 1))) break;
+      if (GATHER && nb == 0 && valid) a.part_ml[(size_t)item.part * 256 + t * 128 + r] = make_float2(-INFINITY, 0.f);
+      if (nt > 0 && (nb > 0 || !partial)) {
+        if (nb > 0) {
+          if (!(ok = wait(o_done(t), (done + nb - 1) & 1))) break;
           tc_fence_after();
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -753,7 +780,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         if (partial && valid) a.part_ml[prow] = make_float2(m * sl, l);
         __nv_bfloat16* o = (__nv_bfloat16*)a.o + (size_t)(item.q0 + t0 + tl) * a.so +
                            (size_t)(item.kh * group + r % group) * HD;
-        const bool poison = nh > 0 && *(volatile int*)&sb.poison[it & 3] == it + 1;
+        const bool poison = nb > 0 && *(volatile int*)&sb.poison[it & 3] == it + 1;
         // keys of mixed blocks of either tile
         int from, to;
         if constexpr (GATHER) {
@@ -768,7 +795,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           uint32_t x[32];
-          if (nh > 0) {
+          if (nb > 0) {
             tmem_ld32(oc + c, x);
             tmem_wait_ld();
           } else {
@@ -815,7 +842,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         }
         tc_fence_before();  // O is read before the next item's first product overwrites it
       }
-      done += nh;
+      done += nb;
       ub += 2 * sp.n;
     }
   }
@@ -846,7 +873,7 @@ __global__ void __launch_bounds__(256) k_attn_prompt_join(PromptArgs a, int part
   if ((int)threadIdx.x >= ROWS * PER || row >= 256 || r >= tok * a.group || token >= pt.lq) return;
   const PromptItem it = {pt.q0, pt.k0, pt.lq, pt.lk, pt.tile, kh, 0, 0};
   const TcSpan whole = PromptWork::span(it, tok, 1);
-  const int blocks = cdiv(t ? whole.nh[1] : whole.nh[0], 2), chunk = cdiv(whole.n, a.splits);
+  const int blocks = t ? whole.nb[1] : whole.nb[0], chunk = cdiv(whole.n, a.splits);
   // a range's partial, or its two where both tiles took the rows (blocks in turn)
   const int two = whole.nt[1] == 0 ? 2 : 1;
   const size_t p0 = (size_t)pair * a.splits * 256 + row;
