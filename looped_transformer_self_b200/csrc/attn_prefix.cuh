@@ -70,22 +70,12 @@ __device__ __forceinline__ int prefix_group_blocks(const PrefixArgs& a, const Pr
   return n;
 }
 
-__device__ __forceinline__ long long warp_incl_scan(long long v) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  return v;
-}
-
 template <int BN>
 struct PrefixPos {
   PrefixGroup g;
   int gi, kh, mt, nmt;   // group, key/value head, row tile, row tiles of the group
   int t;                 // tile index
-  long long u0;          // first unit of the tile
+  int u0;                // first unit of the tile
   int nb;                // its blocks
   int row0, nrow;        // its rows
   int2 tail;             // its rows' tail entries
@@ -114,73 +104,102 @@ struct PrefixPos {
   }
 };
 
-// CTAs that get units: with fewer units than CTAs, one each (a CTA without units has no part).
-__device__ __forceinline__ int prefix_ctas(long long U, int grid) { return (int)min(U, (long long)grid); }
-__device__ __forceinline__ long long prefix_u0(int c, long long U, int ctas) { return c * U / ctas; }
-__device__ __forceinline__ int prefix_cta_of(long long u, long long U, int ctas) {
-  int c = (int)(u * ctas / U);
+// floor(a b / c) of non-negative numbers; a 32-bit division where the product allows.
+__device__ __forceinline__ int mul_div(int a, int b, int c) {
+  const unsigned long long p = (unsigned long long)(unsigned)a * (unsigned)b;
+  return p >> 32 ? (int)(p / (unsigned)c) : (int)((unsigned)p / (unsigned)c);
+}
+__device__ __forceinline__ int prefix_u0(int c, int U, int ctas) { return mul_div(c, U, ctas); }
+__device__ __forceinline__ int prefix_cta_of(int u, int U, int ctas) {
+  int c = mul_div(u, ctas, U);
   while (c > 0 && prefix_u0(c, U, ctas) > u) --c;
   while (c + 1 < ctas && prefix_u0(c + 1, U, ctas) <= u) ++c;
   return c;
 }
+__device__ __forceinline__ int warp_incl_scan(int v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
 
-
-// The parts of one CTA, walked through by every warp alike.
+// The parts of one CTA, walked through by every warp alike.  The host bounds
+// the units of all tiles by 2^30, so they are counted in 32 bits (the 64-bit
+// divisions and scans of a first form took 4 us of each call).
 template <int BN>
 struct PrefixWalk {
   PrefixPos<BN> pos;
   int b0, n;              // the part's blocks of pos's tile
   int first_cta, n_ctas;  // the tile's CTAs
-  long long u, hi, U;     // units of this CTA, of all (units laid end to end)
-  int ctas;
+  int u, hi, U;           // units of this CTA, of all (units laid end to end)
+  int ctas, scale;        // CTAs with units; the tiles' shares are of `scale` CTAs
   bool own;               // the tiles have CTAs of their own
 
+  // What a lane knows of group s0 + lane; blocks and shares are of one key/value head.
+  struct Group {
+    PrefixGroup g;
+    int nmt, blocks, shares;
+  };
   // CTAs of a tile of nb blocks that has its own.
-  __device__ __forceinline__ int share(int nb, int grid) const { return (int)max(1ll, nb * (long long)grid / U); }
-  __device__ __forceinline__ int group_share(const PrefixArgs& a, const PrefixGroup& g, int tok, int grid) const {
-    int s = 0;
-    for (int i = 0; i < g.m; i += tok) {
-      const int2 t = prefix_tail(a, g.r0 + i, min(tok, g.m - i));
-      s += share(prefix_blocks<BN>(g.np, t.y - t.x), grid);
-    }
-    return s;
+  __device__ __forceinline__ int share(int nb) const { return max(1, mul_div(nb, scale, U)); }
+  __device__ __forceinline__ void load(const PrefixArgs& a, int tok, int s0, Group& x) const {
+    const int g = s0 + (threadIdx.x & 31);
+    x = {{0, 0, 0, 0}, 0, 0, 0};
+    if (g >= a.n_groups) return;
+    x.g = prefix_group(a, g);
+    x.nmt = cdiv(x.g.m, tok);
+    x.blocks = prefix_group_blocks<BN>(a, x.g, tok);
   }
-  // Sets the tile `left` shares (CTAs, or blocks where !own) into the tiles: `left` becomes what
-  // remains within the tile.  False if there is none.
-  __device__ __forceinline__ bool locate(const PrefixArgs& a, int tok, int grid, long long& left) {
-    const int lane = threadIdx.x & 31;
-    long long tiles = 0;
+  __device__ __forceinline__ void set_shares(const PrefixArgs& a, int tok, Group& x) const {
+    x.shares = 0;
+    if (x.nmt == 1) {
+      x.shares = share(x.blocks);
+    } else {
+      for (int i = 0; i < x.g.m; i += tok) {
+        const int2 t = prefix_tail(a, x.g.r0 + i, min(tok, x.g.m - i));
+        x.shares += share(prefix_blocks<BN>(x.g.np, t.y - t.x));
+      }
+    }
+  }
+  __device__ __forceinline__ int sum(int v) const { return (int)__reduce_add_sync(0xffffffffu, (unsigned)v); }
+
+  // Sets the tile `left` (CTAs where the tiles own them, else blocks) into the tiles: `left` becomes
+  // what remains within the tile.  False if there is none.  `first`: the first 32 groups.
+  __device__ __forceinline__ bool locate(const PrefixArgs& a, int tok, const Group& first, int& left) {
+    int tiles = 0;
     pos.u0 = 0;
     for (int s0 = 0; s0 < a.n_groups; s0 += 32) {
-      long long sum = 0, nt = 0, blocks = 0;
-      PrefixGroup pg = {0, 0, 0, 0};
-      if (s0 + lane < a.n_groups) {
-        pg = prefix_group(a, s0 + lane);
-        blocks = (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
-        sum = own ? (long long)a.kv_heads * group_share(a, pg, tok, grid) : blocks;
-        nt = (long long)a.kv_heads * cdiv(pg.m, tok);
+      Group x = first;
+      if (s0 > 0) {
+        load(a, tok, s0, x);
+        if (own) set_shares(a, tok, x);
       }
-      const long long is = warp_incl_scan(sum), it = warp_incl_scan(nt), ib = warp_incl_scan(blocks);
+      const int mine = a.kv_heads * (own ? x.shares : x.blocks), nt = a.kv_heads * x.nmt, nb = a.kv_heads * x.blocks;
+      const int is = warp_incl_scan(mine);
       const unsigned here = __ballot_sync(0xffffffffu, is > left);
+      const int w = here ? __ffs(here) - 1 : 32;  // the group's lane
+      const bool before = (int)(threadIdx.x & 31) < w;
+      tiles += sum(before ? nt : 0);
+      pos.u0 += sum(before ? nb : 0);
       if (here) {
-        const int w = __ffs(here) - 1;
         pos.gi = s0 + w;
-        pos.g.r0 = __shfl_sync(0xffffffffu, pg.r0, w);
-        pos.g.m = __shfl_sync(0xffffffffu, pg.m, w);
-        pos.g.p0 = __shfl_sync(0xffffffffu, pg.p0, w);
-        pos.g.np = __shfl_sync(0xffffffffu, pg.np, w);
-        left -= __shfl_sync(0xffffffffu, is - sum, w);
-        pos.u0 += __shfl_sync(0xffffffffu, ib - blocks, w);
-        pos.t = (int)(tiles + __shfl_sync(0xffffffffu, it - nt, w));
-        const long long per = __shfl_sync(0xffffffffu, sum, w) / a.kv_heads;  // of one head
-        pos.nmt = cdiv(pos.g.m, tok);
-        pos.kh = (int)(left / per);
+        pos.g.r0 = __shfl_sync(0xffffffffu, x.g.r0, w);
+        pos.g.m = __shfl_sync(0xffffffffu, x.g.m, w);
+        pos.g.p0 = __shfl_sync(0xffffffffu, x.g.p0, w);
+        pos.g.np = __shfl_sync(0xffffffffu, x.g.np, w);
+        left -= __shfl_sync(0xffffffffu, is - mine, w);
+        pos.nmt = __shfl_sync(0xffffffffu, x.nmt, w);
+        const int per = __shfl_sync(0xffffffffu, own ? x.shares : x.blocks, w);  // of one head
+        pos.kh = left / per;
         left -= pos.kh * per;
-        pos.t += pos.kh * pos.nmt;
-        pos.u0 += pos.kh * (__shfl_sync(0xffffffffu, blocks, w) / a.kv_heads);
+        pos.t = tiles + pos.kh * pos.nmt;
+        pos.u0 += pos.kh * __shfl_sync(0xffffffffu, x.blocks, w);
         for (pos.mt = 0;; ++pos.mt) {
           pos.set_tile(a, tok);
-          const int here_n = own ? share(pos.nb, grid) : pos.nb;
+          const int here_n = own ? share(pos.nb) : pos.nb;
           if (left < here_n || pos.mt + 1 >= pos.nmt) break;
           left -= here_n;
           pos.u0 += pos.nb;
@@ -189,58 +208,61 @@ struct PrefixWalk {
         return true;
       }
       left -= __shfl_sync(0xffffffffu, is, 31);
-      pos.u0 += __shfl_sync(0xffffffffu, ib, 31);
-      tiles += __shfl_sync(0xffffffffu, it, 31);
     }
     return false;
   }
   __device__ __forceinline__ void set_part() {
-    b0 = (int)(u - pos.u0);
-    n = (int)min((long long)pos.nb - b0, hi - u);
+    b0 = u - pos.u0;
+    n = min(pos.nb - b0, hi - u);
     first_cta = prefix_cta_of(pos.u0, U, ctas);
     n_ctas = prefix_cta_of(pos.u0 + pos.nb - 1, U, ctas) - first_cta + 1;
   }
   // The first part of CTA `cta` of `grid`; false: it has none.
   __device__ __forceinline__ bool start(const PrefixArgs& a, int tok, int cta, int grid) {
-    const int lane = threadIdx.x & 31;
-    long long units = 0, tiles = 0;
-    for (int g = lane; g < a.n_groups; g += 32) {
-      const PrefixGroup pg = prefix_group(a, g);
-      units += (long long)a.kv_heads * prefix_group_blocks<BN>(a, pg, tok);
-      tiles += (long long)a.kv_heads * cdiv(pg.m, tok);
+    Group first, x;
+    load(a, tok, 0, first);
+    int units = first.blocks, tiles = first.nmt;
+    for (int s0 = 32; s0 < a.n_groups; s0 += 32) {
+      load(a, tok, s0, x);
+      units += x.blocks;
+      tiles += x.nmt;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      units += __shfl_xor_sync(0xffffffffu, units, o);
-      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-    }
-    U = units;
+    U = a.kv_heads * sum(units);
+    tiles = a.kv_heads * sum(tiles);
     if (U == 0) return false;
-    // CTAs of their own: at least two per tile on average and fewer than a block would make idle
+    // CTAs of their own: at least two per tile on average and fewer than a block would make idle.
+    // Shares are rounded down: of more CTAs than there are, as long as they fit.
     own = 2 * tiles <= grid && U >= grid;
     if (own) {
-      long long shares = 0;
-      for (int g = lane; g < a.n_groups; g += 32)
-        shares += (long long)a.kv_heads * group_share(a, prefix_group(a, g), tok, grid);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) shares += __shfl_xor_sync(0xffffffffu, shares, o);
-      own = shares <= grid;
+      own = false;
+      for (int k = 4; k >= 3 && !own; --k) {  // of grid * 4 / 3, then of grid
+        scale = k == 4 ? grid * 4 / 3 : grid;
+        if (U < scale) continue;
+        set_shares(a, tok, first);
+        int shares = first.shares;
+        for (int s0 = 32; s0 < a.n_groups; s0 += 32) {
+          load(a, tok, s0, x);
+          set_shares(a, tok, x);
+          shares += x.shares;
+        }
+        own = a.kv_heads * sum(shares) <= grid;
+      }
     }
     if (own) {
-      long long k = cta;
-      if (!locate(a, tok, grid, k)) return false;
-      n_ctas = share(pos.nb, grid);
-      first_cta = cta - (int)k;
-      b0 = (int)(k * pos.nb / n_ctas);
-      n = (int)((k + 1) * pos.nb / n_ctas) - b0;
+      int k = cta;
+      if (!locate(a, tok, first, k)) return false;
+      n_ctas = share(pos.nb);
+      first_cta = cta - k;
+      b0 = mul_div(k, pos.nb, n_ctas);
+      n = mul_div(k + 1, pos.nb, n_ctas) - b0;
       return true;
     }
-    ctas = prefix_ctas(U, grid);
+    ctas = min(U, grid);  // with fewer units than CTAs, one each (a CTA without units has no part)
     if (cta >= ctas) return false;
     u = prefix_u0(cta, U, ctas);
     hi = prefix_u0(cta + 1, U, ctas);
-    long long left = u;
-    if (!locate(a, tok, grid, left)) return false;
+    int left = u;
+    if (!locate(a, tok, first, left)) return false;
     set_part();
     return true;
   }

@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   pdl_wait();
   // rows before the first group or behind the last one are left as they were
   const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
+  const int4 rt = a.row_tab[row];  // asked for together with the offsets
   if (row < first || row >= last) return;
-  const int4 rt = a.row_tab[row];
   const int t = rt.x + (h / a.group) * rt.y, r = rt.z + h % a.group;
   if (t < 0 || t >= a.max_tiles || r < 0 || r >= MT) {  // rows that the offsets do not reach
     set_err(a.status, DEV_BAD_INDEX);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   float M = -INFINITY, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
-  constexpr int B = 8;  // partials in flight
+  constexpr int B = 16;  // partials in flight
   for (int k0 = 0; k0 < parts; k0 += B) {
     float2 ml[B];
     float v[B][PER];
@@ -287,6 +287,8 @@ extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, co
   int mt = prefix_small_tile(dtype, n_rows, n_groups, n_heads / n_kv_heads);
   if (dtype == LT_BF16 && prefix_use_tc(mt, (long long)n_prefix + n_tail, n_kv_heads)) mt = 256;
   const PrefixPlan p = prefix_plan(mt, n_rows, n_groups, n_heads, n_kv_heads, head_dim);
+  // the kernels count blocks of all tiles in 32 bits
+  if ((((long long)n_prefix + n_tail) / PREFIX_N + 1) * p.max_tiles > (1 << 30)) return LT_ERR_SHAPE;
   char* s = (char*)d_scratch;
   PrefixArgs a = {d_q, d_cache, d_o, stride_q, stride_o, d_row_off, d_prefix, d_prefix_off, d_tail,
                   d_tail_off, n_groups, n_rows, n_slots, n_prefix, n_tail, n_heads, n_kv_heads,
