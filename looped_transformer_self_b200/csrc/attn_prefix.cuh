@@ -2,8 +2,8 @@
 //
 // A tile is (group of rows, key/value head, up to MT packed query rows); its
 // keys are the group's prefix slots followed by the tail slots of the tile's
-// own rows, in blocks of BN.  Where each tile can have CTAs of its own, in
-// proportion to its blocks, a CTA takes one range of one tile (leaving a tile
+// own rows, in blocks of BN.  Where each tile can have CTAs of its own, a CTA
+// takes one range of one tile (leaving a tile
 // costs a CTA a start-up and a partial: 14 us of 90 at 27.7 blocks of 512 per
 // CTA).  Otherwise the (tile, block) units of all tiles are laid end to end and
 // CTA c of n takes units [c U / n, (c + 1) U / n).  Lengths are read on the
@@ -135,8 +135,9 @@ struct PrefixWalk {
   int b0, n;              // the part's blocks of pos's tile
   int first_cta, n_ctas;  // the tile's CTAs
   int u, hi, U;           // units of this CTA, of all (units laid end to end)
-  int ctas, scale;        // CTAs with units; the tiles' shares are of `scale` CTAs
-  bool own;               // the tiles have CTAs of their own
+  int ctas;               // CTAs with units
+  int most;               // where the tiles have CTAs of their own: the blocks one takes at most
+  bool own;
 
   // What a lane knows of group s0 + lane; blocks and shares are of one key/value head.
   struct Group {
@@ -144,7 +145,7 @@ struct PrefixWalk {
     int nmt, blocks, shares;
   };
   // CTAs of a tile of nb blocks that has its own.
-  __device__ __forceinline__ int share(int nb) const { return max(1, mul_div(nb, scale, U)); }
+  __device__ __forceinline__ int share(int nb) const { return cdiv(nb, most); }
   __device__ __forceinline__ void load(const PrefixArgs& a, int tok, int s0, Group& x) const {
     const int g = s0 + (threadIdx.x & 31);
     x = {{0, 0, 0, 0}, 0, 0, 0};
@@ -155,8 +156,8 @@ struct PrefixWalk {
   }
   __device__ __forceinline__ void set_shares(const PrefixArgs& a, int tok, Group& x) const {
     x.shares = 0;
-    if (x.nmt == 1) {
-      x.shares = share(x.blocks);
+    if (x.nmt <= 1) {
+      x.shares = share(x.blocks);  // none for an empty group
     } else {
       for (int i = 0; i < x.g.m; i += tok) {
         const int2 t = prefix_tail(a, x.g.r0 + i, min(tok, x.g.m - i));
@@ -230,14 +231,12 @@ struct PrefixWalk {
     U = a.kv_heads * sum(units);
     tiles = a.kv_heads * sum(tiles);
     if (U == 0) return false;
-    // CTAs of their own: at least two per tile on average and fewer than a block would make idle.
-    // Shares are rounded down: of more CTAs than there are, as long as they fit.
-    own = 2 * tiles <= grid && U >= grid;
-    if (own) {
-      own = false;
-      for (int k = 4; k >= 3 && !own; --k) {  // of grid * 4 / 3, then of grid
-        scale = k == 4 ? grid * 4 / 3 : grid;
-        if (U < scale) continue;
+    // CTAs of their own where the tiles are few: the longest part as short as the CTAs allow, to
+    // within a few blocks.
+    own = false;
+    if (2 * tiles <= grid)
+      for (int more = 0; more <= 16 && !own; more = more ? 2 * more : 1) {
+        most = cdiv(U, grid) + more;
         set_shares(a, tok, first);
         int shares = first.shares;
         for (int s0 = 32; s0 < a.n_groups; s0 += 32) {
@@ -247,7 +246,6 @@ struct PrefixWalk {
         }
         own = a.kv_heads * sum(shares) <= grid;
       }
-    }
     if (own) {
       int k = cta;
       if (!locate(a, tok, first, k)) return false;
