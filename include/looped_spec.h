@@ -408,8 +408,10 @@ int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y
  * All three are asynchronous on `stream` (of the current device), allocate
  * nothing, copy nothing from the host and may be captured in a CUDA graph:
  * lengths and offsets are read on the device when the kernels run, so a
- * replayed graph follows them.  A scratch buffer belongs to one call (or one
- * captured graph) at a time; its contents need no initialisation.
+ * replayed graph follows them.  A scratch buffer (32-byte aligned) belongs to one
+ * call (or one captured graph) at a time; its contents need no initialisation.
+ * Outputs must not overlap inputs.  Each kernel starts its set-up while the work
+ * before it on the stream drains and touches global memory after that.
  * Offset arrays ("_off", device int32 [n + 1]) are ascending: entry i is
  * off[i] .. off[i+1] - 1, empty entries are allowed.
  * d_status (device int32, zeroed by the caller, may be NULL) receives the
@@ -434,7 +436,8 @@ int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y
  * that a query does not see never reaches it, infinities and NaN included.
  * Errors: LT_ERR_ARG (null pointer, negative size, bad dtype, scale not
  * positive and finite, a stride below the row), LT_ERR_SHAPE (heads, head_dim,
- * a base or stride that is not a multiple of 16 bytes, a grid over 2^31 tiles),
+ * a base or stride that is not a multiple of 16 bytes, scratch not 32-byte
+ * aligned, a grid over 2^31 tiles),
  * LT_ERR_CAPACITY (scratch), LT_ERR_CUDA (launch).
  */
 int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int n_heads, int n_kv_heads,
@@ -462,7 +465,8 @@ int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, const void* d
  *   d_tail_off int32 [n_rows + 1]
  * Rows outside the groups are left as they were.  A value that a row does not
  * see never reaches it, infinities and NaN included.
- * Errors: as lt_attn_prompt; LT_ERR_SHAPE also for n_rows over 65535.
+ * Errors: as lt_attn_prompt; LT_ERR_SHAPE also for n_rows over 65535 and for
+ * more than 2^30 blocks of 64 keys in all (tiles of rows times listed keys).
  */
 int lt_attn_prefix_scratch_bytes(int dtype, int n_rows, int n_groups, int n_heads, int n_kv_heads,
                                  int head_dim, size_t* bytes);

@@ -237,11 +237,11 @@ static int prefix_small_tile(int dtype, int n_rows, int n_groups, int group) {
 }
 // The tensor-core tiles (256 packed rows) cost about 4 us more to start and less per key; the more
 // rows the few-rows kernel holds, the fewer keys it takes to make that up.  Measured at head size 128
-// (few rows / tiles): 16 heads, 1 row, 6000 keys 26.2 / 28.1 us, 20000 keys 48.8 / 45.3; 32 rows,
-// 1000 keys 15.3 / 18.1, 2500 keys 23.7 / 22.9, 20000 keys 58.7 / 45.8; 32 heads on 8, 32 rows, 2500
-// keys 28.0 / 25.6, 20000 keys 75.3 / 42.4.
+// (few rows / tiles, us): 16 heads, 1 row, 2500 keys 13.2 / 17.6, 6000 keys 21.8 / 23.0, 20000 keys
+// 48.2 / 42.2; 32 rows, 1000 keys 15.4 / 15.9, 2500 keys 17.1 / 17.6, 6000 keys 28.3 / 23.2; 32 heads
+// on 8, 32 rows (128 packed), 300 keys 14.3 / 13.8, 2500 keys 22.8 / 19.5, 20000 keys 74.8 / 37.5.
 static bool prefix_use_tc(int mt, long long keys, int n_kv_heads) {
-  return keys * n_kv_heads >= (mt == 64 ? 24000 : mt == 32 ? 48000 : 160000);
+  return keys * n_kv_heads >= (mt == 64 ? 8000 : mt == 32 ? 48000 : 160000);
 }
 
 }  // namespace lt
@@ -281,7 +281,7 @@ extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, co
   const long long w = (long long)n_heads * head_dim;
   if (stride_q < w || stride_o < w) return LT_ERR_ARG;
   if (!attn_aligned(dtype, d_q, stride_q) || !attn_aligned(dtype, d_o, stride_o) ||
-      ((uintptr_t)d_cache & 15) || ((uintptr_t)d_scratch & 15))
+      ((uintptr_t)d_cache & 15) || ((uintptr_t)d_scratch & 31))
     return LT_ERR_SHAPE;
   if (scratch_bytes < need) return LT_ERR_CAPACITY;
   int mt = prefix_small_tile(dtype, n_rows, n_groups, n_heads / n_kv_heads);

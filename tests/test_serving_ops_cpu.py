@@ -28,7 +28,7 @@ def _prompt(**kw):
     (dict(scale=float("nan")), ARG), (dict(hd=48), SHAPE), (dict(hd=256), SHAPE), (dict(Hk=3), SHAPE),
     (dict(Hk=0), SHAPE), (dict(H=130, Hk=2, sq=130 * 128, so=130 * 128), SHAPE), (dict(q=None), ARG),
     (dict(k=None), ARG), (dict(v=None), ARG), (dict(o=None), ARG), (dict(qo=None), ARG),
-    (dict(scratch=None), ARG), (dict(sq=511), ARG), (dict(sk=255), ARG), (dict(sv=255), ARG),
+    (dict(scratch=None), ARG), (dict(scratch=P + 16), SHAPE), (dict(sq=511), ARG), (dict(sk=255), ARG), (dict(sv=255), ARG),
     (dict(so=504), ARG), (dict(sq=516), SHAPE), (dict(sk=260), SHAPE), (dict(q=P + 8), SHAPE),
     (dict(v=P + 2), SHAPE), (dict(o=P + 4), SHAPE), (dict(bytes=0), CAPACITY),
     (dict(n_q=2**31 - 1, H=64, Hk=1, sq=64 * 128, so=64 * 128), SHAPE),
@@ -53,7 +53,7 @@ def _prefix(**kw):
     (dict(o=None), ARG), (dict(ro=None), ARG), (dict(prefix=None), ARG), (dict(po=None), ARG),
     (dict(tail=None), ARG), (dict(to=None), ARG), (dict(scratch=None), ARG), (dict(sq=500), ARG),
     (dict(so=8), ARG), (dict(sq=513), SHAPE), (dict(cache=P + 8), SHAPE), (dict(o=P + 8), SHAPE),
-    (dict(scratch=P + 4), SHAPE), (dict(bytes=1000), CAPACITY), (dict(n_rows=0), 0), (dict(n_groups=0), 0),
+    (dict(scratch=P + 4), SHAPE), (dict(scratch=P + 16), SHAPE), (dict(n_prefix=2**31 - 1, n_rows=4000), SHAPE), (dict(bytes=1000), CAPACITY), (dict(n_rows=0), 0), (dict(n_groups=0), 0),
 ])
 def test_prefix_refusals(kw, code):
     assert _prefix(**kw) == code
