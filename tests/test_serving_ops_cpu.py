@@ -67,7 +67,8 @@ def _verify(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(n=-1), ARG), (dict(k=-1), ARG), (dict(V=0), ARG), (dict(p=None), ARG), (dict(sp=99), ARG),
+    (dict(n=-1), ARG), (dict(k=-1), ARG), (dict(V=0), ARG),
+    (dict(V=2**30 + 1, sp=2**31, sq=2**31), ARG), (dict(p=None), ARG), (dict(sp=99), ARG),
     (dict(sq=99), ARG), (dict(x=None), ARG), (dict(off=None), ARG), (dict(ua=None), ARG),
     (dict(ud=None), ARG), (dict(acc=None), ARG), (dict(tok=None), ARG), (dict(n=0), 0),
 ])
