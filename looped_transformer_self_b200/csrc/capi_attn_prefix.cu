@@ -8,8 +8,8 @@
 namespace lt {
 
 // fp32 arithmetic throughout (CUDA cores): the form of fp32 models.  Bound by
-// its start, the partition and one block's chain where the cache is short (two
-// groups on 777 shared slots, 4 heads of 32: 12.8 us with the merge).
+// its start, the partition and one block's chain where the cache is short (2 and
+// 9 rows on 777 and 289 shared slots, 4 heads of 32: 13 us with the merge).
 template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs a) {
   extern __shared__ __align__(16) char smem_raw[];
