@@ -438,6 +438,37 @@ def test_verify_strides_and_bad_offsets():
     assert acc.tolist() == [want[0][0], -1] and int(status) == 4
 
 
+@pytest.mark.parametrize("onehot", [False, True])
+@pytest.mark.parametrize("n,V", [(460, 33003), (200, 20000), (70, 4097)])
+def test_verify_many_chains_with_infinities(n, V, onehot):
+    """One, two and four CTAs a chain, several segments and groups a warp; entries that weigh nothing."""
+    lens = [i % 2 for i in range(n)]
+    p, q, x, ua, ud = _verify_inputs(lens, V, n, onehot)
+    g = torch.Generator().manual_seed(n)
+    for bad in (float("inf"), float("nan"), -float("inf")):
+        rows = torch.arange(0, p.shape[0], 3)
+        p[rows, torch.randint(V, rows.shape, generator=g)] = bad
+        if q is not None:
+            rows = torch.arange(0, q.shape[0], 2)
+            q[rows, torch.randint(V, rows.shape, generator=g)] = bad
+    ud[:4] = torch.tensor([0.0, 1 - 2.0 ** -24, 0.5, 1 - 2.0 ** -24])
+    got = _verify_call(p, q, x, lens, ua, ud)
+    assert got == R.verify(p, q, x.tolist(), _off(lens, "cpu").tolist(), ua, ud)
+
+
+def test_verify_long_rows():
+    """More segments than one round of a group's warps, and rows past 2^24 bytes."""
+    V, lens = 9_000_001, [1, 0]
+    g = torch.Generator().manual_seed(9)
+    p = torch.rand(3, V, generator=g)
+    p /= p.sum(-1, keepdim=True)
+    x = torch.tensor([V - 5], dtype=torch.int32)
+    for u in (0.0, 0.37, 0.83, 1 - 2.0 ** -24):
+        ua, ud = torch.ones(1), torch.tensor([u, (u + 0.1) % 1])
+        got = _verify_call(p, None, x, lens, ua, ud)
+        assert got == R.verify(p, None, x.tolist(), [0, 1, 1], ua, ud)
+
+
 # ---- together -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
