@@ -107,6 +107,12 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
   } while (walk.next(a, tok));
 }
 
+// N consecutive values, moved at once where N is a power of two.
+template <typename T, int N>
+struct alignas(N == 3 ? sizeof(T) : N * sizeof(T)) MergeVec {
+  T x[N];
+};
+
 // Merge of a row's partials: with M the largest m, o = sum_i 2^(m_i - M) O_i /
 // sum_i 2^(m_i - M) l_i.  One warp per (row, head); bound by
 // its chain of table, maxima and partials (3 us, 5 us for 19 partials of 64 rows of 32
@@ -138,14 +144,14 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   constexpr int B = 16;  // partials in flight
   for (int k0 = 0; k0 < parts; k0 += B) {
     float2 ml[B];
-    float v[B][PER];
+    MergeVec<float, PER> v[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       const bool there = k0 + k < parts;
       const size_t p = (size_t)(tt.x + (k0 + k) / two + t) * MT + (k0 + k) % two * (MT / 2) + r;
       ml[k] = there ? a.part_ml[p] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) v[k][i] = there ? a.part[p * HD + lane * PER + i] : 0.f;
+      v[k] = {};
+      if (there) v[k] = *reinterpret_cast<const MergeVec<float, PER>*>(a.part + p * HD + lane * PER);
     }
     float mx = M;
 #pragma unroll
@@ -161,13 +167,14 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
       const float w = ex2(ml[k].x - ms);
       l += w * ml[k].y;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[k][i], o[i]);
+      for (int i = 0; i < PER; ++i) o[i] = fmaf(w, v[k].x[i], o[i]);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* dst = (T*)a.o + (size_t)row * a.so + (size_t)h * HD + lane * PER;
+  MergeVec<T, PER> out;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) dst[i] = from_f<T>(o[i] * inv);
+  for (int i = 0; i < PER; ++i) out.x[i] = from_f<T>(o[i] * inv);
+  *reinterpret_cast<MergeVec<T, PER>*>((T*)a.o + (size_t)row * a.so + (size_t)h * HD + lane * PER) = out;
 }
 
 template <typename T, int HD, int MT>
