@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   auto give_back = [&](int it) { mbar_arrive(smem_u32(&sb.item_empty[it % TC_ITEMS])); };
 
   // Registers a thread: 168 at launch with three warps per scheduler, of which the softmax
-  // warpgroups take 216 and the third keeps 72 (216 + 216 + 72 = 3 * 168); 128 with four, 200, 200,
-  // 56 and 56 (= 4 * 128).
+  // warpgroups take 216 and the third keeps 72 (216 + 216 + 72 = 3 * 168); 128 with four, 192, 192,
+  // 72 and 56 (= 4 * 128; 200, 200, 56 and 56 spilled in the third: 1 % slower).
   if (GATHER && warp >= 12) {
     if constexpr (GATHER) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
     }
   } else if (warp >= 8) {
     if constexpr (GATHER)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
     }
   } else {
     if constexpr (GATHER)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int t = warp >> 2, r = threadIdx.x & 127;
