@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
   const uint32_t smem = smem_u32(smem_raw);
   const int group = a.group, tok = MT / group;
   pdl_trigger();
+  pdl_wait();
   PrefixWalk<PREFIX_N> walk;
   if (!walk.start(a, tok, blockIdx.x, gridDim.x)) return;
   const PrefixPos<PREFIX_N>& pos = walk.pos;
