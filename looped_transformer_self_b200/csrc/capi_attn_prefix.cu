@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
     for (int i = 0; i < PER; ++i) o[i] *= f;
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      if (ml[k].x == -INFINITY) continue;  // a partial that saw nothing has no outputs
+      // A partial that saw nothing has no outputs.  NaN scores alone leave no maximum either, but a NaN
+      // sum, which has to reach the row.
+      if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
       const float w = ex2(ml[k].x - ms);
       l += w * ml[k].y;
 #pragma unroll
