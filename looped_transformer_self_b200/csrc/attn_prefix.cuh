@@ -40,6 +40,28 @@ struct PrefixArgs {
   int* status;
 };
 
+// What the merge takes from the tables for one (row, head).  Entries that no CTA wrote hold whatever the
+// scratch held (offsets that are not as promised, a wait that gave up), so nothing is assumed of them.
+struct PrefixPlace {
+  int t, r;             // tile, packed row in it
+  int first, parts, two;  // first CTA, partials in all, partials of a part
+};
+__host__ __device__ __forceinline__ bool prefix_place(int4 row, int head, int group, int max_tiles, int mt,
+                                                      PrefixPlace& p) {
+  const long long t = row.x + (long long)(head / group) * row.y, r = (long long)row.z + head % group;
+  p.two = row.w == 2 ? 2 : 1;
+  if (t < 0 || t >= max_tiles || row.z < 0 || r >= (p.two == 2 ? mt / 2 : mt)) return false;
+  p.t = (int)t;
+  p.r = (int)r;
+  return true;
+}
+__host__ __device__ __forceinline__ bool prefix_parts(int4 tile, int grid, PrefixPlace& p) {
+  if (tile.x < 0 || tile.x >= grid || tile.y <= 0 || tile.y > grid - tile.x) return false;
+  p.first = tile.x;
+  p.parts = tile.y * p.two;
+  return true;
+}
+
 struct PrefixGroup {
   int r0, m, p0, np;
 };

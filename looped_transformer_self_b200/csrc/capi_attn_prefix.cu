@@ -127,28 +127,22 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
   const int4 rt = a.row_tab[row];  // asked for together with the offsets
   if (row < first || row >= last) return;
-  const int t = rt.x + (h / a.group) * rt.y, r = rt.z + h % a.group;
-  if (t < 0 || t >= a.max_tiles || r < 0 || r >= MT) {  // rows that the offsets do not reach
-    set_err(a.status, DEV_BAD_INDEX);
+  PrefixPlace at;
+  if (!prefix_place(rt, h, a.group, a.max_tiles, MT, at) || !prefix_parts(a.tile_tab[at.t], grid, at)) {
+    set_err(a.status, DEV_BAD_INDEX);  // rows that the offsets do not reach
     return;
   }
-  const int4 tt = a.tile_tab[t];
-  if (tt.x < 0 || tt.y <= 0 || tt.x + tt.y > grid) {
-    set_err(a.status, DEV_BAD_INDEX);
-    return;
-  }
-  const int two = rt.w == 2 ? 2 : 1, parts = tt.y * two;
   float M = -INFINITY, l = 0.f, o[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = 0.f;
   constexpr int B = 16;  // partials in flight
-  for (int k0 = 0; k0 < parts; k0 += B) {
+  for (int k0 = 0; k0 < at.parts; k0 += B) {
     float2 ml[B];
     MergeVec<float, PER> v[B];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const bool there = k0 + k < parts;
-      const size_t p = (size_t)(tt.x + (k0 + k) / two + t) * MT + (k0 + k) % two * (MT / 2) + r;
+      const bool there = k0 + k < at.parts;
+      const size_t p = (size_t)(at.first + (k0 + k) / at.two + at.t) * MT + (k0 + k) % at.two * (MT / 2) + at.r;
       ml[k] = there ? a.part_ml[p] : make_float2(-INFINITY, 0.f);
       v[k] = {};
       if (there) v[k] = *reinterpret_cast<const MergeVec<float, PER>*>(a.part + p * HD + lane * PER);
