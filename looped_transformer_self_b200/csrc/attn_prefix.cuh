@@ -149,8 +149,8 @@ __device__ __forceinline__ int warp_incl_scan(int v) {
 }
 
 // The parts of one CTA, walked through by every warp alike.  The host bounds
-// the units of all tiles by 2^30, so they are counted in 32 bits (the 64-bit
-// divisions and scans of a first form took 4 us of each call).
+// the units of as many tiles as the scratch holds by 2^30, so they are counted in
+// 32 bits (the 64-bit divisions and scans of a first form took 4 us of each call).
 template <int BN>
 struct PrefixWalk {
   PrefixPos<BN> pos;
@@ -188,6 +188,10 @@ struct PrefixWalk {
     }
   }
   __device__ __forceinline__ int sum(int v) const { return (int)__reduce_add_sync(0xffffffffu, (unsigned)v); }
+  // The same of numbers up to 2^31 - 1 whose sum may pass 32 bits.
+  __device__ __forceinline__ long long sum_wide(int v) const {
+    return ((long long)sum(v >> 16) << 16) + sum(v & 0xffff);
+  }
 
   // Sets the tile `left` (CTAs where the tiles own them, else blocks) into the tiles: `left` becomes
   // what remains within the tile.  False if there is none.  `first`: the first 32 groups.
@@ -244,14 +248,22 @@ struct PrefixWalk {
   __device__ __forceinline__ bool start(const PrefixArgs& a, int tok, int cta, int grid) {
     Group first, x;
     load(a, tok, 0, first);
-    int units = first.blocks, tiles = first.nmt;
+    unsigned units = first.blocks;
+    int nmt = first.nmt;
     for (int s0 = 32; s0 < a.n_groups; s0 += 32) {
       load(a, tok, s0, x);
       units += x.blocks;
-      tiles += x.nmt;
+      nmt = min(nmt + x.nmt, a.max_tiles + 1);
     }
-    U = a.kv_heads * sum(units);
-    tiles = a.kv_heads * sum(tiles);
+    // Groups that overlap make more tiles than the scratch has room for, and more units than 32 bits
+    // count: none of them is worked on.
+    const long long all = a.kv_heads * sum_wide(nmt);
+    if (all > a.max_tiles) {
+      if ((threadIdx.x & 31) == 0) set_err(a.status, DEV_BAD_INDEX);
+      return false;
+    }
+    const int tiles = (int)all;
+    U = a.kv_heads * sum((int)units);
     if (U == 0) return false;
     // CTAs of their own where the tiles are few: the longest part as short as the CTAs allow, to
     // within a few blocks.

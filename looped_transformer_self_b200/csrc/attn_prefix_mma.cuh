@@ -69,10 +69,6 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
   const size_t width = (size_t)a.kv_heads * HD;
   const float sl = a.scale * 1.4426950408889634f;  // scores in log2 units
   do {
-    if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
-      set_err(a.status, DEV_BAD_INDEX);
-      return;
-    }
     walk.publish(a, threadIdx.x, C::THREADS);
     const int b0 = walk.b0, b1 = b0 + walk.n;
     const int rows = pos.nrow * group;

@@ -551,10 +551,6 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         if (walk.start(a, rows, blockIdx.x, gridDim.x)) {
           do {
             const PrefixPos<128>& pos = walk.pos;
-            if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
-              set_err(a.status, DEV_BAD_INDEX);
-              break;
-            }
             walk.publish(a, lane, 32, tok, pos.nrow <= tok);
             if (!hand_over(it, PrefixItem{pos.row0, pos.nrow, pos.g.p0, pos.g.np, pos.tail.x,
                                           pos.g.np + pos.tail.y - pos.tail.x, walk.b0, walk.n, 0, pos.kh,

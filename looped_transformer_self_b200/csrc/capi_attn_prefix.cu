@@ -25,10 +25,6 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
   const size_t width = (size_t)a.kv_heads * HD;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   do {
-    if (pos.t >= a.max_tiles) {  // groups that overlap: more tiles than the scratch has room for
-      set_err(a.status, DEV_BAD_INDEX);
-      return;
-    }
     walk.publish(a, threadIdx.x, SIMT_THREADS);
     const int b0 = walk.b0, b1 = b0 + walk.n;
     const int rows = pos.nrow * group, h0 = pos.kh * group;
