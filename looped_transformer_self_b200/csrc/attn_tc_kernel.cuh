@@ -671,7 +671,8 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         if (mixed) {
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
-          // that see them at the end.  A thread goes over one key's row.
+          // that see them at the end.  A thread goes over one key's row.  Every thread
+          // fences: a row that it finds clean may have been cleaned by the other tile a moment before.
           const int u = ub + 2 * jr + 1;
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
           char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;
@@ -700,8 +701,8 @@ __global__ void __launch_bounds__(W::THREADS, 1)
               drop_nonfinite(v.w);
               *q = v;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         float mx4[4];
 #pragma unroll

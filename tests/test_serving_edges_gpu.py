@@ -68,3 +68,59 @@ def test_overlapping_groups_that_fit_keep_the_other_rows(dtype, keys):
                          32 ** -0.5)
     assert int(status) == 4
     assert bool(((got[5:, 0].double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("H,Hk,hd,rows,n,most", [(32, 4, 128, 30, 6000, 9), (64, 2, 96, 8, 14000, 60),
+                                                 (8, 2, 64, 60, 12345, 20)])
+def test_bad_tail_values_with_two_tiles_on_one_block(H, Hk, hd, rows, n, most, bad):
+    """Both tiles of a call on the tensor-core tiles go over the same value rows; a bad value in each fourth
+    row's tail reaches that row alone, run after run."""
+    from looped_transformer_self_b200.binding import attn_prefix
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    r = random.Random(rows)
+    assert (H // Hk) * rows > 128
+    nt = [r.randint(1, most) for _ in range(rows)]
+    cache = torch.randn(n + sum(nt), 2, Hk * hd, generator=g, device="cuda").bfloat16()
+    q = torch.randn(rows, H, hd, generator=g, device="cuda").bfloat16()
+    order = list(range(n + sum(nt)))
+    r.shuffle(order)
+    tails = [[order.pop() for _ in range(m)] for m in nt]
+    want, tol = R.prefix(q, cache, [rows], [order], tails, hd ** -0.5)
+    hit = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    for i in range(0, rows, 4):
+        cache[tails[i][-1], 1] = bad
+        hit[i] = True
+    args = (q, cache, _i32([0, rows]), _i32(order), _i32([0, n]), _i32([s for t in tails for s in t]), _off(nt))
+    whole = None
+    for _ in range(25):
+        got = attn_prefix(*args)
+        assert not bool(got[hit].isfinite().any())
+        assert bool(((got[~hit].double() - want[~hit]).abs() <= tol[~hit]).all())
+        bits = got.view(torch.int16)
+        assert whole is None or torch.equal(bits, whole)
+        whole = bits.clone()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_bad_values_of_the_last_block_with_two_tiles_on_it(bad):
+    """A prompt whose two tiles end in the same block: a bad value at every fourth key of it."""
+    from looped_transformer_self_b200.binding import attn_prompt
+    H, Hk, hd, lq = 16, 2, 128, 30
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn(lq, H, hd, generator=g, device="cuda").bfloat16()
+    k, v = (torch.randn(lq, Hk, hd, generator=g, device="cuda").bfloat16() for _ in range(2))
+    want, tol = R.prompt(q, k, v, [lq], [lq], hd ** -0.5)
+    for i in range(14, lq, 4):
+        v[i, :, i] = bad
+    off, whole = _off([lq]), None
+    reached = torch.zeros(lq, H, hd, dtype=torch.bool, device="cuda")
+    for i in range(14, lq, 4):
+        reached[i:, :, i] = True
+    for _ in range(25):
+        got = attn_prompt(q, k, v, off)
+        assert not bool(got[reached].isfinite().any())
+        assert bool(((got.double() - want).abs() <= tol)[~reached].all())
+        bits = got.view(torch.int16)
+        assert whole is None or torch.equal(bits, whole)
+        whole = bits.clone()
