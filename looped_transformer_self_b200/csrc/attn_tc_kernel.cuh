@@ -624,11 +624,11 @@ __global__ void __launch_bounds__(W::THREADS, 1)
       const int t0 = t ? sp.t0[1] : sp.t0[0], nt = t ? sp.nt[1] : sp.nt[0], nb = t ? sp.nb[1] : sp.nb[0];
       const bool valid = tl < nt && r < tok * group;
       // Keys a row sees: [0, see) and, of the slot cache, also [own.x, own.y).  Keys from `shared` on
-      // are not seen by all rows of the tile.
-      int see, shared;
+      // are not seen by all rows of the tile, keys from `scanned` on not by all rows of both tiles.
+      int see, shared, scanned;
       int2 own = {0, 0};
       if constexpr (GATHER) {
-        see = shared = item.np;
+        see = shared = scanned = item.np;
         if (valid) {
           const int2 t2 = off_range(a.tail_off, item.q0 + t0 + tl, a.n_tail, a.status);
           own = {item.np + t2.x - item.tail0, item.np + t2.y - item.tail0};
@@ -637,6 +637,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
         const int ctx = item.lk - item.lq;
         see = valid ? ctx + t0 + tl + 1 : 0;  // may be <= 0
         shared = ctx + t0 + 1;
+        scanned = ctx + sp.t0[0] + 1;
       }
       float m = -INFINITY, l = 0.f;                   // m: reference maximum of the raw scores
       for (int jj = 0; jj < nb; ++jj) {
@@ -668,11 +669,13 @@ __global__ void __launch_bounds__(W::THREADS, 1)
               if (!(seen & (1u << i))) x[c * 32 + i] = 0xff800000u;  // -inf
           }
         }
-        if (mixed) {
+        if ((j + 1) * 128 > scanned) {
           // Values that some row must not see: rows behind the keys (other sequences, padding)
           // are zeroed, infinities and NaN taken out (0 * inf is NaN) and given back to the rows
-          // that see them at the end.  A thread goes over one key's row.  Every thread
-          // fences: a row that it finds clean may have been cleaned by the other tile a moment before.
+          // that see them at the end.  A thread goes over one key's row.  Both tiles do this for the
+          // same blocks, each before its own product, so that neither multiplies what the other may
+          // have taken out or not; and every thread fences, since a row that it finds clean may have
+          // been cleaned by the other tile a moment before.
           const int u = ub + 2 * jr + 1;
           if (!(ok = wait(kv_full(slot_of(u)), par_of(u)))) break;
           char* row = smem_raw + (2 + slot_of(u)) * C::TILE + r * 128;

@@ -124,3 +124,43 @@ def test_bad_values_of_the_last_block_with_two_tiles_on_it(bad):
         bits = got.view(torch.int16)
         assert whole is None or torch.equal(bits, whole)
         whole = bits.clone()
+
+
+@pytest.mark.parametrize("H,Hk,hd,lq,ctx", [(16, 16, 128, 256, 0), (55, 55, 96, 500, 0), (8, 2, 64, 640, 70),
+                                            (4, 1, 128, 40, 3000), (6, 6, 32, 1000, 64)])
+def test_infinities_in_blocks_that_one_tile_sees_whole(H, Hk, hd, lq, ctx):
+    """Infinite values at keys that lie before all rows of a pair's second tile and among those of its first.
+    Rows that do not see them are untouched; rows that do, however small their weight, are infinite, in every
+    run alike."""
+    from looped_transformer_self_b200.binding import attn_prompt
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    lk = lq + ctx
+    q = torch.randn(lq, H, hd, generator=g, device="cuda").bfloat16()
+    k = torch.randn(lk, Hk, hd, generator=g, device="cuda").bfloat16()
+    v = torch.randn(lk, Hk, hd, generator=g, device="cuda").bfloat16()
+    want, tol = R.prompt(q, k, v, [lq], [lk], hd ** -0.5)
+    tok = 128 // (H // Hk)
+    at = ctx + tok // 2  # in the first tile's diagonal block
+    first = at - ctx     # the first row that sees it
+    v[at, :, 5] = float("inf")
+    off, koff = _off([lq]), _off([lk])
+    for far in (False, True):
+        if far:  # a score far below the row's maximum: the weight is 0 in fp32
+            q[:, :, 0] = 30.0
+            k[:, :, 0] = 30.0
+            k[at, :, 0] = -30.0
+            want, tol = R.prompt(q, k, v.nan_to_num(posinf=0.0), [lq], [lk], hd ** -0.5)
+        whole = None
+        for _ in range(25):
+            got = attn_prompt(q, k, v, off, koff)
+            clean = got[:first].double()
+            assert not bool(((clean - want[:first]).abs() > tol[:first]).any()) and bool(clean.isfinite().all())
+            near = got[first:2 * tok, :, 5]  # rows of the pair: both tiles take the value out and give it back
+            assert bool(near.isposinf().all())
+            assert not bool(got[first:, :, 5].isfinite().any())
+            rest = torch.cat([got[first:, :, :5], got[first:, :, 6:]], -1).double()
+            other = torch.cat([want[first:, :, :5], want[first:, :, 6:]], -1)
+            assert bool(((rest - other).abs() <= torch.cat([tol[first:, :, :5], tol[first:, :, 6:]], -1)).all())
+            bits = got.view(torch.int16)
+            assert whole is None or torch.equal(bits, whole)
+            whole = bits.clone()
