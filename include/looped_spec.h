@@ -437,7 +437,7 @@ int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y
  * Errors: LT_ERR_ARG (null pointer, negative size, bad dtype, scale not
  * positive and finite, a stride below the row), LT_ERR_SHAPE (heads, head_dim,
  * a base or stride that is not a multiple of 16 bytes, scratch not 32-byte
- * aligned, a grid over 2^31 tiles),
+ * aligned, a grid over 2^31 tiles, more than 2^31 - 1024 queries or keys),
  * LT_ERR_CAPACITY (scratch), LT_ERR_CUDA (launch).
  */
 int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int n_heads, int n_kv_heads,
@@ -466,7 +466,8 @@ int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, const void* d
  * Rows outside the groups are left as they were.  A value that a row does not
  * see never reaches it, infinities and NaN included.
  * Errors: as lt_attn_prompt; LT_ERR_SHAPE also for n_rows over 65535 and for
- * more than 2^30 blocks of 64 keys in all (tiles of rows times listed keys).
+ * more than 2^30 blocks of 64 keys in all (tiles of rows times listed keys) or
+ * 2^31 - 1024 listed keys.
  */
 int lt_attn_prefix_scratch_bytes(int dtype, int n_rows, int n_groups, int n_heads, int n_kv_heads,
                                  int head_dim, size_t* bytes);
@@ -499,7 +500,7 @@ int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, const void* d
  *   d_tokens int32 [n_drafts + n_seqs]: chain s from off[s] + s on: its accepted
  *       drafts, the drawn token (-1 if the row has no mass), then -1
  * Errors: LT_ERR_ARG (null pointer, negative size, V <= 0 or over 2^30, a stride
- * below V),
+ * below V, more than 2^31 - 1024 drafts and chains),
  * LT_ERR_CUDA (launch).
  */
 int lt_verify_drafts(const float* d_p, long long stride_p, const float* d_q, long long stride_q,

@@ -13,6 +13,7 @@
 namespace lt {
 
 constexpr int ATTN_MAX_GROUP = 64;  // query heads per key/value head (they share a 64-row tile)
+constexpr int COUNT_MAX = 0x7fffffff - 1023;  // rows or keys: kernels count some blocks past them in 32 bits
 
 __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 

@@ -277,6 +277,7 @@ extern "C" int lt_attn_prefix(int dtype, const void* d_q, long long stride_q, co
   const int e = lt_attn_prefix_scratch_bytes(dtype, n_rows, n_groups, n_heads, n_kv_heads, head_dim, &need);
   if (e != LT_OK) return e;
   if (n_slots < 0 || n_prefix < 0 || n_tail < 0 || !(scale > 0.f) || !(scale < INFINITY)) return LT_ERR_ARG;
+  if ((long long)n_prefix + n_tail > COUNT_MAX) return LT_ERR_SHAPE;
   if (n_rows == 0 || n_groups == 0) return LT_OK;
   if (!d_q || !d_o || !d_row_off || !d_prefix_off || !d_tail_off || !d_scratch ||
       (n_slots > 0 && !d_cache) || (n_prefix > 0 && !d_prefix) || (n_tail > 0 && !d_tail))

@@ -110,7 +110,7 @@ extern "C" int lt_attn_prompt_scratch_bytes(int dtype, int n_q, int n_seqs, int 
   if (!bytes || (dtype != LT_F32 && dtype != LT_BF16) || n_q < 0 || n_seqs < 0) return LT_ERR_ARG;
   if (!attn_shape_ok(n_heads, n_kv_heads, head_dim)) return LT_ERR_SHAPE;
   // the launch grid counts tiles of at least 64 / group tokens
-  if (((long long)n_q / (SIMT_M / (n_heads / n_kv_heads)) + n_seqs) * n_kv_heads > 0x7fffffff)
+  if (n_q > COUNT_MAX || ((long long)n_q / (SIMT_M / (n_heads / n_kv_heads)) + n_seqs) * n_kv_heads > 0x7fffffff)
     return LT_ERR_SHAPE;
   *bytes = 256;
   if (dtype == LT_BF16) {
@@ -133,6 +133,7 @@ extern "C" int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, co
   if (!attn_shape_ok(n_heads, n_kv_heads, head_dim)) return LT_ERR_SHAPE;
   size_t need = 0;
   if (int e = lt_attn_prompt_scratch_bytes(dtype, n_q, n_seqs, n_heads, n_kv_heads, head_dim, &need)) return e;
+  if (n_kv > COUNT_MAX) return LT_ERR_SHAPE;
   if (n_seqs == 0 || n_q == 0) return LT_OK;
   if (!d_q || !d_o || !d_q_off || !d_scratch || (n_kv > 0 && (!d_k || !d_v))) return LT_ERR_ARG;
   const long long w = (long long)n_heads * head_dim, wk = (long long)n_kv_heads * head_dim;

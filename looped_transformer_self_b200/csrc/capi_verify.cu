@@ -327,7 +327,7 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
                                 int V, const float* d_u_accept, const float* d_u_draw,
                                 int32_t* d_n_accepted, int32_t* d_tokens, int32_t* d_status,
                                 void* stream) {
-  if (n_seqs < 0 || n_drafts < 0 || V <= 0 || V > (1 << 30) || (long long)n_drafts + n_seqs > 0x7fffffff) return LT_ERR_ARG;
+  if (n_seqs < 0 || n_drafts < 0 || V <= 0 || V > (1 << 30) || (long long)n_drafts + n_seqs > COUNT_MAX) return LT_ERR_ARG;
   if (n_seqs == 0) return LT_OK;
   if (!d_p || !d_off || !d_u_draw || !d_n_accepted || !d_tokens || stride_p < V ||
       (n_drafts > 0 && (!d_draft || !d_u_accept)) || (d_q && stride_q < V))
