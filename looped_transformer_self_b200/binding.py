@@ -254,9 +254,16 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _launch(dev: int, stream, what, fn, *args) -> None:
-    """fn(*args, stream handle) with device `dev` current."""
-    handle = (torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+def _launch(dev: int, stream, tensors, what, fn, *args) -> None:
+    """fn(*args, stream handle) with device `dev` current.  Memory of `tensors` that is freed
+    is not given out again before their work on a given stream has ended."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
     if dev == torch._C._cuda_getDevice():
         code = fn(*args, handle)
     else:
@@ -339,8 +346,9 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_off: torch.
     if scratch is None:
         scratch = attn_prompt_scratch(q, k, q_off, stream)
     sc, sc_bytes = _list(scratch, "scratch", torch.uint8, dev)
-    _launch(dev, stream, "lt_attn_prompt", lib().lt_attn_prompt, _DTYPE[dt], q.data_ptr(), sq, k.data_ptr(),
-            sk, v.data_ptr(), sv, out.data_ptr(), so, qo, ko, n - 1, n_q, n_kv, H, Hk, hd,
+    _launch(dev, stream, (q, k, v, q_off, kv_off, out, scratch, status), "lt_attn_prompt",
+            lib().lt_attn_prompt, _DTYPE[dt], q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv,
+            out.data_ptr(), so, qo, ko, n - 1, n_q, n_kv, H, Hk, hd,
             hd ** -0.5 if scale is None else scale, sc, sc_bytes, _status_ptr(status, dev))
     return out
 
@@ -380,7 +388,8 @@ def attn_prefix(q: torch.Tensor, cache: torch.Tensor, row_off: torch.Tensor, pre
     if scratch is None:
         scratch = attn_prefix_scratch(q, cache, row_off, stream)
     sc, sc_bytes = _list(scratch, "scratch", torch.uint8, dev)
-    _launch(dev, stream, "lt_attn_prefix", lib().lt_attn_prefix, _DTYPE[dt], q.data_ptr(), sq,
+    _launch(dev, stream, (q, cache, row_off, prefix, prefix_off, tail, tail_off, out, scratch, status),
+            "lt_attn_prefix", lib().lt_attn_prefix, _DTYPE[dt], q.data_ptr(), sq,
             cache.data_ptr(), n_slots, out.data_ptr(), so, ro, n - 1, n_rows, pre, po, n_prefix, tl, to,
             n_tail, H, width // hd, hd, hd ** -0.5 if scale is None else scale, sc, sc_bytes,
             _status_ptr(status, dev))
@@ -410,8 +419,9 @@ def verify_drafts(p: torch.Tensor, q, drafts: torch.Tensor, off: torch.Tensor,
         assert q_shape == (k, V), "q: another shape than wanted"
         qp = q.data_ptr()
     acc, tok = _new(n, _I32, p.device, stream), _new(k + n, _I32, p.device, stream)
-    _launch(dev, stream, "lt_verify_drafts", lib().lt_verify_drafts, p.data_ptr(), sp, qp, sq, x, of, n, k,
-            V, ua, ud, acc.data_ptr(), tok.data_ptr(), _status_ptr(status, dev))
+    _launch(dev, stream, (p, q, drafts, off, u_accept, u_draw, status), "lt_verify_drafts",
+            lib().lt_verify_drafts, p.data_ptr(), sp, qp, sq, x, of, n, k, V, ua, ud, acc.data_ptr(),
+            tok.data_ptr(), _status_ptr(status, dev))
     return acc, tok
 
 

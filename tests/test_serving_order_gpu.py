@@ -155,3 +155,33 @@ def test_captured_chain_follows_new_inputs(dtype, hd):
             g.replay()
         side.synchronize()
         assert torch.equal(out, wants[i % 3]), i
+
+
+def test_inputs_freed_behind_a_call_on_a_given_stream():
+    """The given stream is busy when the call is made; its inputs are freed at once and their memory is asked
+    for again on the current stream."""
+    from looped_transformer_self_b200.binding import attn_prefix, attn_prompt, verify_drafts
+    qkv, cache = _inputs("bf16", 11)
+    lists, off = _lists(), _i32([0, N])
+    g = torch.Generator(device="cuda").manual_seed(12)
+    ver = [torch.rand(5, 4000, generator=g, device="cuda"), torch.rand(4, 4000, generator=g, device="cuda"),
+           torch.randint(4000, (4,), generator=g, device="cuda", dtype=torch.int32), _i32([0, 4]),
+           torch.rand(4, generator=g, device="cuda"), torch.rand(1, generator=g, device="cuda")]
+    torch.cuda.synchronize()
+    want = [attn_prompt(*qkv, off), attn_prefix(qkv[0, :ROWS], cache, **lists), *verify_drafts(*ver)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        t = [x.clone() for x in qkv] + [off.clone()]
+        c, ls, vs = cache.clone(), {k: x.clone() for k, x in lists.items()}, [x.clone() for x in ver]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+        got = [attn_prompt(*t, stream=side), attn_prefix(t[0][:ROWS], c, **ls, stream=side),
+               *verify_drafts(*vs, stream=side)]
+        sizes = [x.shape for x in [*t, c, *ls.values(), *vs]], [x.dtype for x in [*t, c, *ls.values(), *vs]]
+        del t, c, ls, vs
+        reused = [torch.zeros(s, dtype=d, device="cuda") for s, d in zip(*sizes)]
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del reused
