@@ -409,7 +409,8 @@ int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y
  * nothing, copy nothing from the host and may be captured in a CUDA graph:
  * lengths and offsets are read on the device when the kernels run, so a
  * replayed graph follows them.  A scratch buffer (32-byte aligned) belongs to one
- * call (or one captured graph) at a time; its contents need no initialisation.
+ * call (or one captured graph) at a time; its contents need no initialisation, and
+ * the functions that size it answer for the current device.
  * Outputs must not overlap inputs.  Each kernel starts its set-up while the work
  * before it on the stream drains and touches global memory after that.
  * Offset arrays ("_off", device int32 [n + 1]) are ascending: entry i is

@@ -254,6 +254,14 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _on_device(dev: int, fn, *args) -> int:
+    """fn(*args) with device `dev` current."""
+    if dev == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _launch(dev: int, stream, tensors, what, fn, *args) -> None:
     """fn(*args, stream handle) with device `dev` current.  Memory of `tensors` that is freed
     is not given out again before their work on a given stream has ended."""
@@ -264,11 +272,7 @@ def _launch(dev: int, stream, tensors, what, fn, *args) -> None:
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
-    if dev == torch._C._cuda_getDevice():
-        code = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args, handle)
+    code = _on_device(dev, fn, *args, handle)
     if code != 0:
         raise LoopedSpecError(code, what)
 
@@ -305,7 +309,7 @@ def _status_ptr(status, dev: int):
 
 def _scratch(need_fn, dtype, device, stream, *sizes) -> torch.Tensor:
     need = _sz()
-    check(need_fn(dtype, *sizes, ctypes.byref(need)), "scratch bytes")
+    check(_on_device(device.index, need_fn, dtype, *sizes, ctypes.byref(need)), "scratch bytes")
     return _new(need.value, torch.uint8, device, stream)
 
 

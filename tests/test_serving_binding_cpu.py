@@ -111,3 +111,15 @@ def test_current_stream_needs_no_record(world, name):
     call(None)
     assert all(not t.recorded for t in tensors)
     assert lib.calls[-1][2][-1] == 5
+
+
+@pytest.mark.parametrize("name", ["prompt", "prefix"])
+@pytest.mark.parametrize("stream", [None, FakeStream()])
+def test_scratch_is_sized_for_the_tensors_device(world, name, stream):
+    """The bytes depend on the device's processors: they are asked for with the tensors' device current,
+    as the launch is made, and the current device is left as it was."""
+    B, lib, cuda = world
+    _, call = _make(B, 1, name)
+    call(stream)
+    assert [(n, d) for n, d, _ in lib.calls] == [(f"lt_attn_{name}_scratch_bytes", 1), (f"lt_attn_{name}", 1)]
+    assert lib.calls[-1][2][-3] == 1001 and cuda["current"] == 0
