@@ -164,3 +164,91 @@ def test_infinities_in_blocks_that_one_tile_sees_whole(H, Hk, hd, lq, ctx):
             bits = got.view(torch.int16)
             assert whole is None or torch.equal(bits, whole)
             whole = bits.clone()
+
+
+def _spot(q, cache, rows, prefixes, tails, got, n, r):
+    """Some rows one by one against 64 bits."""
+    first, hd = [sum(rows[:g]) for g in range(len(rows))], q.shape[2]
+    for i in sorted(r.sample(range(sum(rows)), min(n, sum(rows)))):
+        g = max(k for k in range(len(rows)) if first[k] <= i and rows[k])
+        want, tol = R.prefix(q[i:i + 1], cache, [1], [prefixes[g]], [tails[i]], hd ** -0.5)
+        assert bool(((got[i:i + 1].double() - want).abs() <= tol).all()), (i, g)
+
+
+# groups: one row each (independent requests), rows of several tiles, empty groups in rows of their own
+GROUPS = [([1] * 256, 40, 3), ([1] * 33, 700, 1), ([0] * 32 + [5, 0, 1] + [0] * 40 + [2], 300, 4),
+          ([70, 0, 1] * 23, 90, 2), ([1] * 1000, 9, 2), ([3] * 64 + [0] * 64 + [200], 130, 5)]
+
+
+@pytest.mark.parametrize("dtype,H,Hk,hd", [("bf16", 16, 16, 128), ("bf16", 8, 2, 64), ("bf16", 32, 2, 96),
+                                           ("f32", 4, 2, 32)])
+@pytest.mark.parametrize("rows,np_,most", GROUPS)
+def test_more_groups_than_a_warp(dtype, H, Hk, hd, rows, np_, most):
+    """More than 32 groups: the partition goes over them in steps."""
+    from looped_transformer_self_b200.binding import attn_prefix
+    r = random.Random(len(rows) + hd)
+    g = torch.Generator(device="cuda").manual_seed(len(rows))
+    lens = [r.randint(0, np_) for _ in rows]
+    nt = [r.randint(1, most) for _ in range(sum(rows))]
+    slots = 2 * max(np_, 2000)
+    prefixes = [[r.randrange(-1, slots) for _ in range(n)] for n in lens]
+    tails = [[r.randrange(slots) for _ in range(n)] for n in nt]
+    cache = torch.randn(slots, 2, Hk * hd, generator=g, device="cuda").to(DT[dtype])
+    q = torch.randn(sum(rows), H, hd, generator=g, device="cuda").to(DT[dtype])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (q, cache, _off(rows), _i32([s for p in prefixes for s in p]), _off(lens),
+            _i32([s for t in tails for s in t]), _off(nt))
+    got = attn_prefix(*args, status=status)
+    assert int(status) == 0
+    _spot(q, cache, rows, prefixes, tails, got, 25, r)
+    assert torch.equal(got, attn_prefix(*args))
+
+
+@pytest.mark.parametrize("dtype,H,Hk,hd", [("bf16", 16, 16, 128), ("bf16", 8, 2, 64), ("f32", 4, 2, 32)])
+@pytest.mark.parametrize("n,most,ctx", [(33, 300, 0), (200, 40, 0), (100, 1, 500), (64, 260, 9), (500, 3, 2)])
+def test_more_sequences_than_a_warp(dtype, H, Hk, hd, n, most, ctx):
+    """More than 32 prompts, empty ones among them: a tile's sequence is found in steps."""
+    from looped_transformer_self_b200.binding import attn_prompt
+    r = random.Random(n + most)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    lq = [r.randint(0, most) if i % 3 else most for i in range(n)]
+    lk = [a + r.randint(0, ctx) if a else 0 for a in lq]
+    q = torch.randn(sum(lq), H, hd, generator=g, device="cuda").to(DT[dtype])
+    k, v = (torch.randn(sum(lk), Hk, hd, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = attn_prompt(q, k, v, _off(lq), _off(lk), status=status)
+    assert int(status) == 0
+    qo, ko = [sum(lq[:i]) for i in range(n)], [sum(lk[:i]) for i in range(n)]
+    for i in r.sample([i for i in range(n) if lq[i]], 12) + [max(j for j in range(n) if lq[j])]:
+        a, b = slice(qo[i], qo[i] + lq[i]), slice(ko[i], ko[i] + lk[i])
+        want, tol = R.prompt(q[a], k[b], v[b], [lq[i]], [lk[i]], hd ** -0.5)
+        assert bool(((got[a].double() - want).abs() <= tol).all()), i
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_on_a_decoders_own_plane(dtype):
+    """The cache that a decode filled, plane by plane: the committed prefix's slots as the shared list, the
+    last ones as the rows' own."""
+    import synthetic as syn
+    from looped_transformer_self_b200.binding import Decoder
+    cfg = syn.MODELS["tiny"] if dtype == "f32" else syn.ModelConfig(
+        "bf16_hd128", "bf16", 256, 2, 128, 512, 1000, 0, 3, 0, 4, resid_scale=0.5, head_gain=4.0, seed=7)
+    dec = Decoder(cfg, syn.DecodeConfig(1, 2, 0.0, 1.0, 2, 32), syn.make_weights(cfg), max_branches=16, max_ctx=400)
+    dec.prefill(syn.uniform_prompt(150, cfg.vocab, 1))
+    dec.generate(20)
+    slots = [x for x in dec.read_committed()[1][:-1] if x >= 0]
+    assert len(slots) >= 150
+    pool, p0 = dec.kv_pool()
+    hd = cfg.d_model // cfg.n_heads
+    g = torch.Generator(device="cuda").manual_seed(1)
+    from looped_transformer_self_b200.binding import attn_prefix
+    for plane in (p0, p0 + cfg.R - 1, p0 + cfg.n_core * cfg.R - 1):
+        cache = pool[plane]
+        q = torch.randn(3, cfg.n_heads, hd, generator=g, device="cuda").to(cache.dtype)
+        prefix, tails = slots[:-3], [slots[-3:-2], slots[-3:-1], slots[-3:]]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = attn_prefix(q, cache, _i32([0, 3]), _i32(prefix), _i32([0, len(prefix)]),
+                          _i32([s for t in tails for s in t]), _off([1, 2, 3]), status=status)
+        want, tol = R.prefix(q, cache, [3], [prefix], tails, hd ** -0.5)
+        assert int(status) == 0 and bool(want.abs().amax() > 0)
+        assert bool(((got.double() - want).abs() <= tol).all())
