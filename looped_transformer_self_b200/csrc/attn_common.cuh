@@ -19,8 +19,8 @@ __host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) 
 
 // The element range of entry i of an offset array, clamped into [0, n] and
 // ascending.  Offsets that had to be clamped are reported once in `status`.
-__device__ __forceinline__ int2 off_range(const int32_t* __restrict__ off, int i, int n, int* status) {
-  const int a = __ldg(off + i), b = __ldg(off + i + 1);
+__device__ __forceinline__ int2 off_range(const int32_t* off, int i, int n, int* status) {
+  const int a = off[i], b = off[i + 1];
   int2 r = {min(max(a, 0), n), min(max(b, 0), n)};
   r.y = max(r.x, r.y);
   if (r.x != a || r.y != b) set_err(status, DEV_BAD_INDEX);
@@ -200,7 +200,9 @@ inline bool attn_shape_ok(int n_heads, int n_kv_heads, int head_dim) {
          n_heads / n_kv_heads <= ATTN_MAX_GROUP;
 }
 // Launches with programmatic dependence on the work before it on the stream: the kernel may start
-// while that drains, and waits for it (pdl_wait) before it reads or writes global memory.
+// while that drains, and waits for it (pdl_wait) before it reads or writes global memory.  What it reads
+// may be written while it already runs, so its loads are ordinary ones: __ldg is for memory that nothing
+// writes in a kernel's lifetime, and the compiler may move it in front of the wait.
 template <typename... P, typename... A>
 inline cudaError_t launch_pdl(void (*kernel)(P...), unsigned grid_x, unsigned grid_y, int threads, size_t smem,
                               cudaStream_t st, const A&... args) {

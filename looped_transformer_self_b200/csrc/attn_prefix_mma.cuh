@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
       const int x = b * PREFIX_N + (int)threadIdx.x;
       int s = -1;
       if (b < b1) {
-        if (x < np) s = __ldg(a.prefix + pos.g.p0 + x);
-        else if (x < nk) s = __ldg(a.tail + pos.tail.x + x - np);
+        if (x < np) s = a.prefix[pos.g.p0 + x];
+        else if (x < nk) s = a.tail[x - np + pos.tail.x];
       }
       return s >= 0 && s < a.n_slots ? s : -1;
     };
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(128, 2) k_attn_prefix_mma(PrefixArgs a) {
       for (int x = max(b0, np / PREFIX_N) * PREFIX_N; x < min(b1 * PREFIX_N, nk); ++x) {
         const int c = x % PREFIX_N;
         if (c / C::KEYS != wk) continue;
-        const int s = x < np ? __ldg(a.prefix + pos.g.p0 + x) : __ldg(a.tail + pos.tail.x + x - np);
+        const int s = x < np ? a.prefix[pos.g.p0 + x] : a.tail[x - np + pos.tail.x];
         if (s < 0 || s >= a.n_slots) continue;
         const __nv_bfloat16* v = kc + ((size_t)s * 2 + 1) * width + gc;
 #pragma unroll

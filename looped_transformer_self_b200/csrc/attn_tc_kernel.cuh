@@ -336,8 +336,8 @@ __global__ void __launch_bounds__(W::THREADS, 1)
           const int x = (item.jb + j) * 128 + w * 32 + lane;
           int s = -1;
           if (j < item.n) {
-            if (x < item.np) s = __ldg(a.prefix + item.p0 + x);
-            else if (x < item.nk) s = __ldg(a.tail + item.tail0 + x - item.np);
+            if (x < item.np) s = a.prefix[item.p0 + x];
+            else if (x < item.nk) s = a.tail[x - item.np + item.tail0];
           }
           return s >= 0 && s < a.n_slots ? s : -1;
         };
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
               if (sp.step == 2 && (((key >> 7) - sp.jb) & 1) != t) continue;  // the other tile's
               const __nv_bfloat16* v;
               if constexpr (GATHER) {
-                const int slot = key < item.np ? __ldg(a.prefix + item.p0 + key) : __ldg(a.tail + item.tail0 + key - item.np);
+                const int slot = key < item.np ? a.prefix[item.p0 + key] : a.tail[key - item.np + item.tail0];
                 if (slot < 0 || slot >= a.n_slots) continue;
                 v = (const __nv_bfloat16*)a.cache + ((size_t)slot * 2 + 1) * a.kv_heads * HD;
               } else {

@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs
       const int x = b * PREFIX_N + threadIdx.x;
       int s = -1;
       if (threadIdx.x < PREFIX_N && b < b1) {
-        if (x < np) s = __ldg(a.prefix + pos.g.p0 + x);
-        else if (x < nk) s = __ldg(a.tail + pos.tail.x + x - np);
+        if (x < np) s = a.prefix[pos.g.p0 + x];
+        else if (x < nk) s = a.tail[x - np + pos.tail.x];
       }
       return s >= 0 && s < a.n_slots ? s : -1;
     };
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) k_attn_prefix_merge(PrefixArgs a, int gri
   if (h >= a.heads) return;
   pdl_wait();
   // rows before the first group or behind the last one are left as they were
-  const int first = max(__ldg(a.row_off), 0), last = min(__ldg(a.row_off + a.n_groups), a.n_rows);
+  const int first = max(*a.row_off, 0), last = min(a.row_off[a.n_groups], a.n_rows);
   const int4 rt = a.row_tab[row];  // asked for together with the offsets
   if (row < first || row >= last) return;
   PrefixPlace at;

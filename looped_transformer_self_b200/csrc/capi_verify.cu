@@ -47,23 +47,23 @@ __device__ __forceinline__ int seg_index(int base, int k) {
   return VEC ? base + (k >> 2) * 128 + lane * 4 + (k & 3) : base + k * 32 + lane;
 }
 template <bool VEC>
-__device__ __forceinline__ void seg_raw(const float* __restrict__ p, int base, int V, float a[16]) {
+__device__ __forceinline__ void seg_raw(const float* p, int base, int V, float a[16]) {
   if (VEC && base + VERIFY_SEG <= V) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p + seg_index<VEC>(base, 4 * i)));
+      const float4 x = *reinterpret_cast<const float4*>(p + seg_index<VEC>(base, 4 * i));
       a[4 * i] = x.x, a[4 * i + 1] = x.y, a[4 * i + 2] = x.z, a[4 * i + 3] = x.w;
     }
   } else {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int j = seg_index<VEC>(base, k);
-      a[k] = j < V ? __ldg(p + j) : 0.f;
+      a[k] = j < V ? p[j] : 0.f;
     }
   }
 }
 template <bool VEC>
-__device__ __forceinline__ void seg_load(const float* __restrict__ p, const float* __restrict__ q, int base,
+__device__ __forceinline__ void seg_load(const float* p, const float* q, int base,
                                          int V, int excl, float w[16]) {
   float b[16];
   seg_raw<VEC>(p, base, V, w);
@@ -75,7 +75,7 @@ __device__ __forceinline__ void seg_load(const float* __restrict__ p, const floa
 }
 // A lane's share of a segment's weights, in 64 bits.
 template <bool VEC>
-__device__ __forceinline__ double seg_sum_exact(const float* __restrict__ p, const float* __restrict__ q, int base,
+__device__ __forceinline__ double seg_sum_exact(const float* p, const float* q, int base,
                                                 int V, int excl) {
   float w[16];
   seg_load<VEC>(p, q, base, V, excl, w);
@@ -86,7 +86,7 @@ __device__ __forceinline__ double seg_sum_exact(const float* __restrict__ p, con
 }
 // The same without the tests of an excluded entry and of infinite weights (then the sum is infinite).
 template <bool VEC>
-__device__ __forceinline__ double seg_sum_fast(const float* __restrict__ p, const float* __restrict__ q, int base,
+__device__ __forceinline__ double seg_sum_fast(const float* p, const float* q, int base,
                                                int V) {
   float a[16], b[16];
   seg_raw<VEC>(p, base, V, a);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS, 3) k_verify(VerifyArgs a, int 
   const int rank = cl.block_rank(), nr = cl.num_blocks();
   const int s = blockIdx.x / nr, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   pdl_wait();
-  const int o0 = __ldg(a.off + s), o1 = __ldg(a.off + s + 1);
+  const int o0 = a.off[s], o1 = a.off[s + 1];
   const bool bad = o0 < 0 || o1 < o0 || o1 > a.n_drafts;  // the same in every CTA of the cluster
   if (bad) {
     if (threadIdx.x == 0 && rank == 0) {
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS, 3) k_verify(VerifyArgs a, int 
     int xi = -1;
     bool ok = i < k;
     if (ok) {
-      xi = __ldg(a.draft + o0 + i);
+      xi = a.draft[o0 + i];
       ok = xi >= 0 && xi < a.V;
       if (ok) {
         const double pv = a.p[(size_t)(o0 + s + i) * a.sp + xi];
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(VERIFY_THREADS, 3) k_verify(VerifyArgs a, int 
   if (rank == 0) {
     const size_t base = (size_t)o0 + s;
     for (int i = threadIdx.x; i <= k; i += VERIFY_THREADS)
-      if (i != acc) a.tok[base + i] = i < acc ? __ldg(a.draft + o0 + i) : -1;
+      if (i != acc) a.tok[base + i] = i < acc ? a.draft[o0 + i] : -1;
     if (threadIdx.x == 0) a.n_acc[s] = acc;
   }
   const float* p = a.p + (size_t)(o0 + s + acc) * a.sp;

@@ -54,3 +54,16 @@ def test_kernel_waits_before_it_touches_global_memory(name):
     for pattern in TOUCHES:
         hit = re.search(pattern, body[:at])
         assert hit is None, f"{name}: {hit.group(0)!r} before the wait"
+
+
+SERVING = ["attn_common.cuh", "attn_prefix.cuh", "attn_prefix_mma.cuh", "attn_tc.cuh", "attn_tc_kernel.cuh",
+           "prompt_tile.cuh", "capi_attn_prefix.cu", "capi_attn_prompt.cu", "capi_verify.cu"]
+
+
+@pytest.mark.parametrize("name", SERVING)
+def test_inputs_are_not_read_as_constant_memory(name):
+    """__ldg (ld.global.nc) asks for memory that nothing writes while the kernel lives.  These kernels start
+    while the work that writes their inputs still runs, and such a load may also move in front of the wait."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    for word in ("__ldg(", "ld.global.nc", "__restrict__"):
+        assert word not in text, word
