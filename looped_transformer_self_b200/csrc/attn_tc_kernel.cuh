@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.group, tok = 128 / group;
-  pdl_trigger();  // what follows may be launched: it waits for this grid's end before it reads
 
   const uint32_t q_s = smem_u32(smem_raw), ring = q_s + 2 * C::TILE;
   const uint32_t q_full = smem_u32(&sb.q_full), q_empty = smem_u32(&sb.q_empty), fin = smem_u32(&sb.fin);
@@ -292,6 +291,9 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // What follows may be launched: it waits for this grid's end before it reads.  Not before this CTA has
+  // its TMEM: a kernel that took the columns first and then waited for this grid would never end.
+  pdl_trigger();
   pdl_wait();
   const uint32_t tmem = sb.tmem;
   auto s_col = [&](int t) { return tmem + (uint32_t)t * 128; };

@@ -67,3 +67,12 @@ def test_inputs_are_not_read_as_constant_memory(name):
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
     for word in ("__ldg(", "ld.global.nc", "__restrict__"):
         assert word not in text, word
+
+
+@pytest.mark.parametrize("name", _launched(_sources()))
+def test_tensor_memory_is_held_before_the_next_kernel_may_start(name):
+    """A next kernel that took tensor memory first and then waited for this one, which waits for the memory,
+    would never end."""
+    body = _body(_sources(), name)
+    at = body.find("pdl_trigger();")
+    assert at < 0 or "tcgen05.alloc" not in body[at:]
