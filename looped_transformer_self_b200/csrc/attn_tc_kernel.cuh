@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(W::THREADS, 1)
   extern __shared__ __align__(1024) char smem_raw[];
   TcSmem<W>& sb = *reinterpret_cast<TcSmem<W>*>(smem_raw + C::TILES);
   if (smem_u32(smem_raw) & 1023) {  // swizzle atoms are 1024 bytes
+    pdl_wait();
     set_err(a.status, DEV_STATE);
     return;
   }

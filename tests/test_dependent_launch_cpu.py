@@ -76,3 +76,10 @@ def test_tensor_memory_is_held_before_the_next_kernel_may_start(name):
     body = _body(_sources(), name)
     at = body.find("pdl_trigger();")
     assert at < 0 or "tcgen05.alloc" not in body[at:]
+
+
+@pytest.mark.parametrize("name", _launched(_sources()))
+def test_no_early_return_without_the_wait(name):
+    """A CTA that reports an error or leaves before the wait would let what follows start too early."""
+    body = _body(_sources(), name)
+    assert "set_err(" not in body[:body.find("pdl_wait();")]
