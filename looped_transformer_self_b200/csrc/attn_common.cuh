@@ -89,9 +89,10 @@ __device__ __forceinline__ void simt_fetch(float* dst, RowPtr row, const float* 
 __device__ __forceinline__ void simt_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void simt_wait1() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// O += P V of one block.  GUARD: a weight of 0 takes nothing from its value
-// row, so that an infinity or NaN in a key that the row does not see stays
-// out (0 * inf is NaN).
+// O += P V of one block.  GUARD: the weight of a key that the row does not see
+// is -0, which takes nothing from its value row, so that an infinity or NaN
+// there stays out (0 * inf is NaN).  A key that it sees with a finite score has a
+// weight of +0 at the least, and its value reaches the row.
 template <int HD, bool GUARD>
 __device__ __forceinline__ void simt_pv(SimtSmem<HD>& sm, SimtState<HD>& st) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
@@ -109,7 +110,7 @@ __device__ __forceinline__ void simt_pv(SimtSmem<HD>& sm, SimtState<HD>& st) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float w = u == 0 ? p[i].x : u == 1 ? p[i].y : u == 2 ? p[i].z : p[i].w;
-          const bool take = !GUARD || w != 0.f;
+          const bool take = !GUARD || (int)__float_as_uint(w) >= 0;  // not -0
           st.o[i][2 * c] = fmaf(w, take ? v.x : 0.f, st.o[i][2 * c]);
           st.o[i][2 * c + 1] = fmaf(w, take ? v.y : 0.f, st.o[i][2 * c + 1]);
         }
@@ -171,7 +172,7 @@ __device__ __forceinline__ void simt_block(SimtSmem<HD>& sm, SimtState<HD>& st, 
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float p = expf(s[i][j] - ms);
+      const float e = expf(s[i][j] - ms), p = masked && s[i][j] == -INFINITY ? -0.f : e;
       sum += p;
       sm.p[r][simt_p_col(r, tx + 16 * j)] = p;
     }

@@ -115,3 +115,45 @@ def test_prompt_nan_query_and_keys(dtype, H, Hk, hd, lq, ctx):
     k[0, Hk - 1, 0] = float("nan")  # seen by the whole first sequence
     nan[:lq[0], (Hk - 1) * (H // Hk):] = True
     _check(attn_prompt(q, k, v, _off(lq), _off(lk)), want, tol, nan)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype,H,Hk,hd,rows,np_,most", SHAPES)
+def test_prefix_bad_value_with_a_vanishing_weight(dtype, H, Hk, hd, rows, np_, most, bad):
+    """A value that a row sees reaches it even where the weight is 0 in fp32: in its own tail, in the last
+    block of the prefix, which holds tails too, and in a block without any."""
+    q, cache, prefixes, tails = _case(dtype, H, Hk, hd, rows, np_, most)
+    kv = cache.view(-1, 2, Hk, hd)
+    q[:, :, 0] = 30.0
+    kv[:, 0, :, 0] = 30.0
+    seen = [tails[1][0], prefixes[0][-1], prefixes[0][0]]
+    kv[seen, 0, :, 0] = -30.0  # scores 1800 / sqrt(hd) below the others
+    want, tol = R.prefix(q, cache, rows, prefixes, tails, hd ** -0.5)
+    hit = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    for i, s in enumerate(seen):
+        kv[s, 1, :, 3 + i] = bad
+        hit[1 if i == 0 else slice(0, rows[0]), :, 3 + i] = True
+    got = _call(q, cache, rows, prefixes, tails)
+    assert not bool(got[hit].isfinite().any())
+    assert bool(((got.double() - want).abs() <= tol)[~hit].all())
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype,H,Hk,hd", [("bf16", 4, 2, 128), ("bf16", 2, 2, 96), ("f32", 4, 2, 64), ("f32", 1, 1, 32)])
+def test_prompt_bad_value_with_a_vanishing_weight(dtype, H, Hk, hd, bad):
+    from looped_transformer_self_b200.binding import attn_prompt
+    g = torch.Generator(device="cuda").manual_seed(hd)
+    n, at = 300, [5, 130, 270]
+    q = torch.randn(n, H, hd, generator=g, device="cuda").to(DT[dtype])
+    k, v = (torch.randn(n, Hk, hd, generator=g, device="cuda").to(DT[dtype]) for _ in range(2))
+    q[:, :, 0] = 30.0
+    k[:, :, 0] = 30.0
+    k[at, :, 0] = -30.0
+    want, tol = R.prompt(q, k, v, [n], [n], hd ** -0.5)
+    hit = torch.zeros(n, H, hd, dtype=torch.bool, device="cuda")
+    for i, s in enumerate(at):
+        v[s, :, 3 + i] = bad
+        hit[s:, :, 3 + i] = True
+    got = attn_prompt(q, k, v, _off([n]))
+    assert not bool(got[hit].isfinite().any())
+    assert bool(((got.double() - want).abs() <= tol)[~hit].all())
