@@ -403,7 +403,9 @@ int lt_gemm_rows_noalloc(int dtype, const void* d_w, const void* d_x, float* d_y
  * reads key/value head h / (n_heads / n_kv_heads), at most 64 query heads per
  * key/value head.  dtype LT_BF16 (bf16 operands and weights of the products,
  * fp32 scores, sums and outputs before the last rounding) or LT_F32 (fp32
- * throughout).
+ * throughout).  An infinite or NaN value that a row sees makes its output
+ * infinite or NaN, a NaN score makes it NaN, and a key whose score is -infinity
+ * counts as not seen.
  *
  * All three are asynchronous on `stream` (of the current device), allocate
  * nothing, copy nothing from the host and may be captured in a CUDA graph:
@@ -454,10 +456,11 @@ int lt_attn_prompt(int dtype, const void* d_q, long long stride_q, const void* d
  * slot cache (LoopSpec page, sections 2.2 and 2.4: the branches of a step
  * attend to the committed prefix and to their own uncommitted positions).
  * Rows row_off[g] .. row_off[g+1]-1 form group g.  Each of them attends to the
- * slots prefix[prefix_off[g] .. prefix_off[g+1]-1], read once for the whole
- * group, and to its own slots tail[tail_off[row] .. tail_off[row+1]-1] (a
- * branch's ancestors and itself; a slot may stand in several rows' tails and
- * more than once).  Slot indices outside 0 .. n_slots-1 (e.g. -1 padding) are
+ * slots prefix[prefix_off[g] .. prefix_off[g+1]-1], read once for a tile of the
+ * group's rows (of 16 to 256 query heads that share a key/value head, by the
+ * group's size and the type), and to its own slots
+ * tail[tail_off[row] .. tail_off[row+1]-1] (a branch's ancestors and itself; a
+ * slot may stand in several rows' tails and more than once).  Slot indices outside 0 .. n_slots-1 (e.g. -1 padding) are
  * skipped.  A row that sees no slot gets zeros.
  *   d_q, d_o   [n_rows][n_heads][head_dim], row stride stride_q / stride_o elements
  *   d_cache    [n_slots][K|V][n_kv_heads * head_dim]: one plane of lt_kv_pool

@@ -6,9 +6,11 @@
 // WM x WK: each holds 16 packed rows and every WK-th 16-key slice of a block,
 // with its own running maximum, sum and output, merged when the CTA leaves the
 // tile.  Rows of shared memory are 16 bytes longer than a cache row, so eight
-// rows' pieces of one column lie in different banks (ldmatrix).  Measured with
-// the merge: 8 rows on 601 shared slots (16 heads of 128, 5.1 MB) 9.7 us, bound
-// by its start and the merge; 1 row on 6000 slots 21.8 us (49 MB, 2.3 TB/s).
+// rows' pieces of one column lie in different banks (ldmatrix).  Weights are
+// rounded to bf16 for their product, as the MMA takes them; their sum is of the
+// fp32 values.  Measured with the merge: 8 rows on 601 shared slots (16 heads of
+// 128, 5.1 MB) 10.0 us, bound by its start and the merge; 1 row on 6000 slots
+// 22.2 us (49 MB, 2.2 TB/s).
 #pragma once
 
 #include "attn_tc_kernel.cuh"

@@ -21,8 +21,9 @@
 //
 // What bounds it: a tile's chain of load S, maximum, 128 exponentials a thread,
 // product and next S, about 3400 cycles per block of both tiles at head size 128
-// against 2048 of the tensor pipe (1536 at 96); the exponentials are 1500 of
-// them.  Measured and not faster: two threads per row (16 softmax warps);
+// against 2048 of the tensor pipe (1536 at 96) and as many of the exponential
+// unit (32768 a block, 16 a cycle; counted on a long prefix: 1045 warp
+// instructions a block, 1024 of them these).  Measured and not faster: two threads per row (16 softmax warps);
 // exponentials on the FMA pipe (polynomial of degree 5); P in halves; half
 // blocks of 64 keys with two S buffers a tile, so that a tile's next S runs
 // under its softmax (11 % faster at head size 96, 5 to 11 % slower at 128 and
@@ -68,7 +69,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 // 32 scores x of a row to weights 2^(x sl + nms), as bf16 pairs in the first half
-// of x, and their fp32 values added to `sum`.
+// of x, and their fp32 values added to `sum`.  The weights are rounded because the
+// product takes both operands in 16 bits; against 64 bits an output is then off by
+// 0.0019 to 0.0023 of its size (rms) where fp32 weights and the one rounding of the
+// output leave 0.0015 to 0.0017.
 __device__ __forceinline__ void softmax_chunk(uint32_t* x, uint64_t sl2, uint64_t nms2, uint64_t* sum) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {

@@ -9,7 +9,9 @@ namespace lt {
 
 // fp32 arithmetic throughout (CUDA cores): the form of fp32 models.  Bound by
 // its start, the partition and one block's chain where the cache is short (2 and
-// 9 rows on 777 and 289 shared slots, 4 heads of 32: 13 us with the merge).
+// 9 rows on 777 and 289 shared slots, 4 heads of 32: 12 to 13 us with the merge).
+// Two CTAs per SM leave 128 registers a thread, which the walk and the tile pass by
+// about 70, 150 and 220 bytes of spills at head sizes 64, 96 and 128.
 template <int HD>
 __global__ void __launch_bounds__(SIMT_THREADS, 2) k_attn_prefix_simt(PrefixArgs a) {
   extern __shared__ __align__(16) char smem_raw[];
@@ -238,11 +240,16 @@ static int prefix_small_tile(int dtype, int n_rows, int n_groups, int group) {
   if (dtype == LT_F32) return SIMT_M;
   return avg <= 16 && group <= 16 ? 16 : avg <= 32 && group <= 32 ? 32 : 64;
 }
-// The tensor-core tiles (256 packed rows) cost about 4 us more to start and less per key; the more
-// rows the few-rows kernel holds, the fewer keys it takes to make that up.  Measured at head size 128
-// (few rows / tiles, us): 16 heads, 1 row, 2500 keys 13.2 / 17.6, 6000 keys 21.8 / 23.0, 20000 keys
-// 48.2 / 42.2; 32 rows, 1000 keys 15.4 / 15.9, 2500 keys 17.1 / 17.6, 6000 keys 28.3 / 23.2; 32 heads
-// on 8, 32 rows (128 packed), 300 keys 14.3 / 13.8, 2500 keys 22.8 / 19.5, 20000 keys 74.8 / 37.5.
+// The tensor-core tiles (256 packed rows) cost up to 4 us more to start and less per key; the more
+// rows the few-rows kernel holds, the fewer keys it takes to make that up.  The sizes are those that the
+// host knows: the lengths of the lists, not what the offsets take of them.  Measured at head size 128
+// (few rows / tiles, us): 16 heads, 1 row, 2500 keys 13.0 / 16.7, 6000 keys 22.2 / 22.4, 10000 keys
+// 30.3 / 29.1, 20000 keys 48.4 / 42.3; 32 rows, 1000 keys 13.8 / 14.1, 2500 keys 16.6 / 17.7, 3500 keys
+// 20.4 / 19.2, 6000 keys 27.4 / 23.2; 64 rows, 400 keys 14.3 / 13.7, 600 keys 14.3 / 14.2; 32 heads on 8,
+// 32 rows (128 packed), 300 keys 14.2 / 13.3, 1000 keys 16.6 / 15.0, 20000 keys 74.1 / 35.4.  Near the
+// bounds the two differ by a microsecond either way.  Smaller heads make fewer bytes of a key, and the
+// tiles come a little early: 1 row of 55 heads of 96, 4000 keys 32.4 / 33.9; 16 heads of 32, 10000 keys
+// 15.2 / 20.7; 8 heads of 64 on 2, 8 rows, 30000 keys 20.2 / 23.8, 80000 keys 32.8 / 33.1.
 static bool prefix_use_tc(int mt, long long keys, int n_kv_heads) {
   return keys * n_kv_heads >= (mt == 64 ? 8000 : mt == 32 ? 48000 : 160000);
 }

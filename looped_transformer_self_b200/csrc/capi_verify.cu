@@ -156,10 +156,11 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // per warp (the running sum decides a token, so its rounding must stay far below
 // a weight); the CTA that holds the crossing reads that one group again, a
 // segment per warp.
-// Bound by HBM for a batch (one row of p and one of q per sequence: 192 chains at
-// 65536 read 100.7 MB in 21.9 us, 7 TB/s beyond the 7.6 us of a call with a short
-// row) and by the chain of dependent loads for one sequence (6.4 us at 49152:
-// offsets, drafts, their probabilities, the row, two barriers, the group again).
+// Bound by HBM for a batch (one row of p and, unless all drafts are accepted, one of
+// q per sequence: 192 chains at 65536, 90 MB read, take 22 us, and 6 us with a row of
+// 64: 5.6 TB/s between the two) and by the chain of dependent loads for one sequence
+// (6.7 us at 49152: offsets, drafts, their probabilities, the row, two barriers, the
+// group again).
 // Testing every entry for the excluded one and for infinities, and a sum per
 // segment, cost 4 us of the batch (25 instructions an entry against 6).
 template <bool VEC>
@@ -332,7 +333,7 @@ extern "C" int lt_verify_drafts(const float* d_p, long long stride_p, const floa
   if (!d_p || !d_off || !d_u_draw || !d_n_accepted || !d_tokens || stride_p < V ||
       (n_drafts > 0 && (!d_draft || !d_u_accept)) || (d_q && stride_q < V))
     return LT_ERR_ARG;
-  // Eight CTAs a sequence for latency (one chain at a vocabulary of 49152: 6.4 us, 6.8 us with four,
+  // Eight CTAs a sequence for latency (one chain at a vocabulary of 49152: 6.4 to 6.7 us, 6.8 us with four,
   // 12.0 us with one), fewer where all of them would not be resident at once with room to place the
   // clusters (148 chains at 65536: 19.2 us with two, 22.7 us with four, which would just fit; 192 chains:
   // 21.9 us with two, 24.6 us with one, 24.8 us with four) or would have less than a segment per warp.
